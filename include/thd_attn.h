@@ -1,7 +1,8 @@
 /*
  * thd_attn.h -- C ABI of the GB300 (sm_103a) packed-THD attention library
- * (forward; its backward and the sparse-attention indexer top-k at the end of
- * this file).
+ * (forward; its backward, the sparse-attention indexer top-k, the per-head norm
+ * with the position rotation, and the paged-cache serving path -- page tables and
+ * one-token attention -- at the end of this file).
  *
  * Operation (scaled-dot-product attention forward with log-sum-exp Stats over a
  * packed, ragged "THD" batch):
@@ -80,7 +81,12 @@ typedef enum { THD_STATS_TOKEN_MAJOR = 0, THD_STATS_HEAD_MAJOR = 1 } thd_stats_l
  * (bf16/fp16, d in {64, 128}, 16-byte aligned rows) and the SIMT kernel
  * otherwise; the other two force one (TCGEN05 fails with THD_ERR_UNSUPPORTED
  * when it does not apply). */
-typedef enum { THD_KERNEL_AUTO = 0, THD_KERNEL_SIMT = 1, THD_KERNEL_TCGEN05 = 2 } thd_kernel_t;
+typedef enum {
+  THD_KERNEL_AUTO = 0,
+  THD_KERNEL_SIMT = 1,
+  THD_KERNEL_TCGEN05 = 2,
+  THD_KERNEL_MMA = 3              /* warp-level matrix instructions; thd_paged_decode only */
+} thd_kernel_t;
 
 /* Mask policy values of the per-sequence mask_type tensor. */
 enum { THD_MASK_NONE = 0, THD_MASK_CAUSAL_TOP_LEFT = 1, THD_MASK_CAUSAL_BOTTOM_RIGHT = 2 };
@@ -92,9 +98,12 @@ enum {
   THD_DEV_BAD_MASK = 1u << 2,       /* mask_type[b] not in {0, 1, 2} */
   THD_DEV_TILE_OVERFLOW = 1u << 3,  /* more work units than the plan's capacity (no work done) */
   THD_DEV_WAIT_TIMEOUT = 1u << 4,   /* a bounded in-kernel wait gave up (kernel returned early) */
-  THD_DEV_KEY_OVERLAP = 1u << 5     /* backward: K or V rows of two sequences overlap without the
+  THD_DEV_KEY_OVERLAP = 1u << 5,    /* backward: K or V rows of two sequences overlap without the
                                        sequences forming one key group (see thd_attn_bwd); no dK
                                        or dV row is written */
+  THD_DEV_BAD_PAGE = 1u << 6,       /* a page number or cache slot outside the cache */
+  THD_DEV_OUT_OF_PAGES = 1u << 7,   /* thd_paged_tables: fewer free pages than the requests need */
+  THD_DEV_BAD_POSITION = 1u << 8    /* a position at or past the end of the rotation table */
 };
 
 /* Host-known problem description, fixed per plan. Index 0..3 of the stride and
@@ -384,6 +393,173 @@ thd_status_t thd_indexer_topk(thd_attn_plan_t plan, const void* q_i, const void*
                               const int32_t* cu_seqlens_kv, const int32_t* off_q, const int32_t* off_k,
                               const int32_t* off_out, const int8_t* mask_type,
                               const int32_t* q_causal_offset, void* workspace, void* stream);
+
+/* ---------------------------------------------- per-head norm and rotation
+ *
+ * What turns the projections of a layer into the Q and K that attention reads: an
+ * RMS norm over each head's d elements and the rotation of its first `rot`
+ * elements by the row's position, in one pass over the data. Per row t of
+ * position p = positions[t], for every head of Q (weight w_q) and of K (w_k):
+ *
+ *     r   = 1 / sqrt(mean_e x_e^2 + eps),   y_e = x_e r w_e
+ *     z_a = y_a c_i - y_b s_i,  z_b = y_b c_i + y_a s_i      i = 0 .. rot/2 - 1
+ *     (a, b) = (i, i + rot/2), or (2i, 2i + 1) with `interleaved`;  z_e = y_e for e >= rot
+ *     c_i = cos_sin[p, i],  s_i = cos_sin[p, rot/2 + i]      (float32 [max_pos, rot])
+ *
+ * All arithmetic is float32; each output is rounded once, to the storage type.
+ * A NULL weight stands for ones. A row whose position is negative is a pad row: it
+ * is skipped, and so is one whose position is >= max_pos (which also sets
+ * THD_DEV_BAD_POSITION). Skipped rows of the outputs are left as they were, or
+ * written as zeros with THD_FLAG_ZERO_SKIPPED.
+ *
+ * Three forms share the descriptor; its views are, by index,
+ *   thd_qk_norm_rope_fwd     0 Q   1 K   2 --     3 Q out   4 K out    5 --
+ *   thd_qk_norm_rope_bwd     0 Q   1 K   2 dQ out 3 dK out  4 dQ       5 dK
+ *   thd_qk_norm_rope_paged   0 Q   1 K   2 V      3 Q out   4 K cache  5 V cache
+ * Views marked -- are ignored. The outputs of fwd (and Q out of paged) may be the
+ * inputs themselves (same pointer and strides), as dQ and dK may be dQ out and dK out;
+ * any other overlap races.
+ */
+typedef enum { THD_NORM_ROPE_FWD = 0, THD_NORM_ROPE_BWD = 1, THD_NORM_ROPE_PAGED = 2 } thd_norm_rope_form_t;
+
+enum { THD_FLAG_ZERO_SKIPPED = 1u << 2 };
+
+typedef struct {
+  thd_dtype_t dtype;              /* every view and both weights */
+  thd_norm_rope_form_t form;
+  int32_t rows;                   /* rows of Q, K (V, outputs, positions, slot_map) */
+  int32_t h_q, h_kv, d;           /* 1 <= d <= 256 */
+  int32_t rot;                    /* rotated elements, even, 0 <= rot <= d */
+  int32_t interleaved;
+  int32_t max_pos;                /* rows of cos_sin */
+  float eps;                      /* >= 0 */
+  int32_t page_size, num_pages;   /* paged form: the cache views are [num_pages, page_size, h_kv, d] */
+  int64_t stride_tok[6];          /* elements; of a cache view: between rows of a page */
+  int64_t stride_head[6];
+  int64_t stride_page[6];         /* cache views only */
+  int64_t bytes[6];               /* allocation behind each pointer; 0 = not checked */
+  uint32_t flags;                 /* THD_FLAG_ZERO_SKIPPED (not for the cache views) */
+} thd_norm_rope_desc_t;
+
+thd_status_t thd_qk_norm_rope_plan(thd_attn_plan_t* out, const thd_norm_rope_desc_t* desc,
+                                   size_t* workspace_bytes);
+
+/* positions: device int32 [rows]. Asynchronous, no allocation, no device->host
+ * read; device data errors surface through thd_attn_read_status. */
+thd_status_t thd_qk_norm_rope_fwd(thd_attn_plan_t plan, const void* q, const void* k, const void* w_q,
+                                  const void* w_k, const float* cos_sin, const int32_t* positions,
+                                  void* q_out, void* k_out, void* workspace, void* stream);
+
+/* Gradients for upstream dQ out and dK out (x is the forward's input, r recomputed):
+ *     g = R(p)^T dz,  a = g w,  xh = x r,  dx = r (a - xh mean_e(a xh)),  dw = sum g xh
+ * dw_q and dw_k are float32 [d], summed over every row and head that is not skipped
+ * in a fixed order (equal inputs give equal bits); either may be NULL. */
+thd_status_t thd_qk_norm_rope_bwd(thd_attn_plan_t plan, const void* q, const void* k, const void* dq_out,
+                                  const void* dk_out, const void* w_q, const void* w_k, const float* cos_sin,
+                                  const int32_t* positions, void* dq, void* dk, float* dw_q, float* dw_k,
+                                  void* workspace, void* stream);
+
+/* The serving form: Q goes to q_out, K (normed and rotated) and V (copied) to row
+ * slot_map[t] of the cache, page slot / page_size, row slot % page_size. A negative
+ * slot writes neither (Q out is still written); one past the cache neither, and sets
+ * THD_DEV_BAD_PAGE. Two rows with one slot race. V is copied for skipped positions
+ * as little as K. */
+thd_status_t thd_qk_norm_rope_paged(thd_attn_plan_t plan, const void* q, const void* k, const void* v,
+                                    const void* w_q, const void* w_k, const float* cos_sin,
+                                    const int32_t* positions, const int32_t* slot_map, void* q_out,
+                                    void* k_cache, void* v_cache, void* workspace, void* stream);
+
+/* -------------------------------------------------------------- page tables
+ *
+ * The cache's bookkeeping for one step, on the device. Request b holds
+ * seq_lens[b] tokens in the pages that its row of block_table names and gets
+ * n_b = cu_new[b+1] - cu_new[b] more (rows cu_new[b] .. of the step's packed rows):
+ *
+ *     old_b = ceil(seq_lens[b] / P),  need_b = ceil((seq_lens[b] + n_b) / P) - old_b
+ *     block_table[b, old_b + i] = free_pages[begin + sum_{a<b} need_a + i]   i < need_b
+ *     row t of b (t = 0 .. n_b - 1): positions = pos = seq_lens[b] + t
+ *                                    slot_map  = block_table[b, pos / P] P + pos % P
+ *     seq_lens_out[b] = seq_lens[b] + n_b,  free_begin_out = begin + sum need
+ *
+ * with (begin, end) = free_span. When the free pages run out (THD_DEV_OUT_OF_PAGES)
+ * the entries and slots that got none are -1, and seq_lens_out counts the tokens
+ * with a page. A request whose seq_lens is negative or which would outgrow its
+ * table row sets THD_DEV_BAD_LENGTH and takes no part: no page, slots and positions
+ * -1, its length unchanged. If cu_new decreases or leaves [0, cap_rows] that holds
+ * for all of them; a free_span outside [0, cap_free] (THD_DEV_BAD_OFFSET) holds no
+ * page. A page number outside the cache, held or free, sets THD_DEV_BAD_PAGE: its
+ * slots are -1 (and the entry, when new). Rows of slot_map and positions that
+ * belong to no request are -1. No other entry of block_table is written.
+ * The inputs seq_lens and free_span are not written, so that a call may be repeated;
+ * a serving loop keeps two of each and swaps them. They must not be the outputs.
+ */
+typedef struct {
+  int32_t batch;                  /* 0 .. 8192 */
+  int32_t page_size;              /* P >= 1 */
+  int32_t num_pages;              /* pages of the cache; num_pages * page_size < 2^31 */
+  int32_t max_pages;              /* columns of block_table; max_pages * page_size < 2^31 */
+  int64_t table_stride;           /* elements between rows of block_table, >= max_pages */
+  int32_t cap_rows;               /* rows of slot_map and positions, <= 2^21 */
+  int32_t cap_free;               /* entries of free_pages */
+  uint32_t flags;                 /* none defined; must be 0 */
+} thd_paged_tables_desc_t;
+
+thd_status_t thd_paged_tables_plan(thd_attn_plan_t* out, const thd_paged_tables_desc_t* desc,
+                                   size_t* workspace_bytes);
+
+/* All arrays are device int32; sizes as in the descriptor, seq_lens and seq_lens_out
+ * [batch], cu_new [batch + 1], free_span [2], free_begin_out [1]. */
+thd_status_t thd_paged_tables(thd_attn_plan_t plan, const int32_t* seq_lens, const int32_t* cu_new,
+                              const int32_t* free_pages, const int32_t* free_span, int32_t* block_table,
+                              int32_t* slot_map, int32_t* positions, int32_t* seq_lens_out,
+                              int32_t* free_begin_out, void* workspace, void* stream);
+
+/* ------------------------------------------- one-token attention over pages
+ *
+ * Attention of one new token per request over its cached keys (the token's own
+ * among them). For request b, query head h (kv head g = h / (h_q / h_kv)), with
+ * n = seq_lens[b] and w = window_left[b]:
+ *
+ *     j visible: max(0, n - 1 - w) <= j < n      (w < 0 or window_left NULL: 0 <= j < n)
+ *     page(j) = block_table[b, j / P],  s_j = softmax_scale <q_bh, K[page(j), j % P, g]>
+ *     Stats = ln sum_j exp(s_j),  O_bh = sum_j exp(s_j - Stats) V[page(j), j % P, g]
+ *
+ * No visible key: O = 0, Stats = -inf. Bytes of the cache outside the visible rows
+ * never reach a result (they may hold NaN). Requests may share pages. A negative
+ * length or one beyond max_pages * page_size sets THD_DEV_BAD_LENGTH and leaves the
+ * request's rows as they were; a page number outside the cache sets
+ * THD_DEV_BAD_PAGE and its keys count as not visible.
+ *
+ * The key range of every (request, kv head) is cut over the whole GPU by its
+ * length, on the device; the partial results are joined in a fixed order by a second
+ * kernel, so equal inputs give equal bits. Calls that overlap on the GPU need a
+ * workspace each.
+ */
+typedef struct {
+  thd_dtype_t dtype;              /* Q, O and both caches */
+  int32_t batch;                  /* rows of Q, O, seq_lens and block_table; 0 .. 8192 */
+  int32_t h_q, h_kv, d;           /* 1 <= d <= 128, h_q % h_kv == 0 */
+  int32_t page_size, num_pages;   /* num_pages * page_size < 2^31 */
+  int32_t max_pages;              /* columns of block_table; max_pages * page_size < 2^31 - 256 */
+  int64_t table_stride;
+  int64_t stride_tok[4];          /* Q, K cache, V cache, O; of a cache: between rows of a page */
+  int64_t stride_head[4];
+  int64_t stride_page[4];         /* caches only */
+  int64_t bytes[4];               /* 0 = not checked */
+  thd_stats_layout_t stats_layout;/* head-major: head stride `batch` */
+  float softmax_scale;            /* NaN => 1/sqrt(d) */
+  thd_kernel_t kernel;            /* AUTO: MMA for bf16/fp16 with d % 8 == 0 and 16-byte cache strides, else SIMT */
+  uint32_t flags;                 /* none defined; must be 0 */
+} thd_paged_decode_desc_t;
+
+thd_status_t thd_paged_decode_plan(thd_attn_plan_t* out, const thd_paged_decode_desc_t* desc,
+                                   size_t* workspace_bytes);
+
+/* stats (float32 [batch * h_q]) and window_left (int32 [batch]) may be NULL. */
+thd_status_t thd_paged_decode(thd_attn_plan_t plan, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_table, const int32_t* seq_lens,
+                              const int32_t* window_left, void* o, float* stats, void* workspace,
+                              void* stream);
 
 #ifdef __cplusplus
 }

@@ -7,6 +7,7 @@ is no fallback -- when the library is missing the first call raises.
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import math
 import os
@@ -14,7 +15,7 @@ import os
 import torch
 
 STATS_TOKEN_MAJOR, STATS_HEAD_MAJOR = 0, 1
-KERNEL_AUTO, KERNEL_SIMT, KERNEL_TCGEN05 = 0, 1, 2
+KERNEL_AUTO, KERNEL_SIMT, KERNEL_TCGEN05, KERNEL_MMA = 0, 1, 2, 3
 FLAG_NO_KV_SPLIT = 1
 FLAG_ELEMENT_OFFSETS = 2
 FLAG_TEST_STALL = 1 << 31
@@ -25,7 +26,7 @@ _STATUS = {0: "THD_OK", 1: "THD_ERR_INVALID_ARG", 2: "THD_ERR_UNSUPPORTED",
 
 # device status word bits
 DEV_BAD_LENGTH, DEV_BAD_OFFSET, DEV_BAD_MASK, DEV_TILE_OVERFLOW, DEV_WAIT_TIMEOUT = 1, 2, 4, 8, 16
-DEV_KEY_OVERLAP = 32
+DEV_KEY_OVERLAP, DEV_BAD_PAGE, DEV_OUT_OF_PAGES, DEV_BAD_POSITION = 32, 64, 128, 256
 
 
 class ThdAttnError(RuntimeError):
@@ -91,7 +92,9 @@ _EXPORTS = ["thd_attn_plan", "thd_attn_fwd", "thd_attn_read_status", "thd_attn_p
             "thd_attn_profile_read", "thd_attn_fwd_static_ws", "thd_attn_static_workspace_capacity",
             "thd_attn_static_read_status",
             "thd_attn_fwd_window", "thd_attn_plan_bwd", "thd_attn_bwd", "thd_indexer_plan",
-            "thd_indexer_topk"]
+            "thd_indexer_topk", "thd_qk_norm_rope_plan", "thd_qk_norm_rope_fwd", "thd_qk_norm_rope_bwd",
+            "thd_qk_norm_rope_paged", "thd_paged_tables_plan", "thd_paged_tables", "thd_paged_decode_plan",
+            "thd_paged_decode"]
 
 
 def library_path() -> str:
@@ -149,6 +152,14 @@ def load_library():
     lib.thd_attn_static_workspace_capacity.restype = ctypes.c_size_t
     lib.thd_attn_static_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
     lib.thd_attn_static_read_status.restype = ctypes.c_int
+    # (plan, tensors..., workspace, stream); the plan makers take (out, descriptor, out)
+    for name, args in (("thd_qk_norm_rope_fwd", 11), ("thd_qk_norm_rope_bwd", 15), ("thd_qk_norm_rope_paged", 14),
+                       ("thd_paged_tables", 12), ("thd_paged_decode", 11)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = [vp] * args, ctypes.c_int
+    for name in ("thd_qk_norm_rope_plan", "thd_paged_tables_plan", "thd_paged_decode_plan"):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = [ctypes.POINTER(vp), vp, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int
     _LIB = lib
     return lib
 
@@ -174,6 +185,15 @@ class ThdAttnPlan:
         if getattr(self, "handle", None) and _LIB is not None:
             _LIB.thd_attn_plan_destroy(self.handle)
             self.handle = None
+
+
+def make_plan(entry: str, desc: ctypes.Structure) -> ThdAttnPlan:
+    """A plan from the library's plan maker of that name."""
+    handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
+    st = getattr(load_library(), entry)(ctypes.byref(handle), ctypes.byref(desc), ctypes.byref(ws))
+    if st != 0:
+        raise ThdAttnError(st, entry)
+    return ThdAttnPlan(handle.value, ws.value, desc)
 
 
 def _view_bytes(t: torch.Tensor) -> int:
@@ -295,6 +315,49 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _enqueue(entry: str, plan: ThdAttnPlan, on: torch.Tensor, tensors, stream) -> None:
+    """Call the library's entry with the tensors' pointers (None: NULL) on ``stream``, or on
+    the current stream of the device that ``on`` lives on, with that device current."""
+    lib = _LIB if _LIB is not None else load_library()
+    dev = on.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    args = [None if t is None else t.data_ptr() for t in tensors]
+    if dev == torch._C._cuda_getDevice():
+        st = getattr(lib, entry)(plan.handle, *args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib, entry)(plan.handle, *args, handle)
+    if st != 0:
+        raise ThdAttnError(st, entry)
+
+
+def _check_ints(name: str, t: torch.Tensor, shape: tuple) -> None:
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _check_devices(first: torch.Tensor, *others) -> None:
+    if first.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if any(t is not None and t.device != first.device for t in others):
+        raise ValueError("tensors must be on one device")
+
+
+def _allocating_on(t: torch.Tensor, stream):
+    """Context in which torch allocates for work on ``stream``: memory that a call takes
+    for itself belongs to the stream that uses it, and is not handed out again before."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
 
 
 def thd_attn_fwd(plan: ThdAttnPlan, q, k, v, o, stats, cu_seqlens_q, cu_seqlens_kv, off_q, off_k,

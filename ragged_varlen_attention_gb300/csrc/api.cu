@@ -58,6 +58,8 @@ bool tc_applicable(const thd_attn_desc_t& d, float scale) {
 
 }  // namespace
 
+int thd::current_device_sms() { return num_sms_of_current_device(); }
+
 extern "C" {
 
 int64_t thd_attn_view_span_bytes(int64_t rows, int64_t heads, int64_t d, int64_t stride_tok,
@@ -270,7 +272,7 @@ thd_status_t thd_attn_fwd_window(thd_attn_plan_t plan, const void* q, const void
                                  const int32_t* off_k, const int32_t* off_v, const int32_t* off_o,
                                  const int32_t* off_s, const int8_t* mask, const int32_t* qco,
                                  const int32_t* window_left, void* workspace, void* stream_ptr) {
-  if (!plan || plan->is_bwd || plan->is_indexer) return THD_ERR_INVALID_ARG;
+  if (!plan || plan->is_bwd || plan->is_indexer || plan->kind) return THD_ERR_INVALID_ARG;
   const thd_attn_desc_t& d = plan->desc;
   if (!workspace) return THD_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) % kAlign != 0) return THD_ERR_WORKSPACE;
@@ -378,6 +380,19 @@ thd_status_t thd_attn_read_status(thd_attn_plan_t plan, const void* workspace, u
   if (!plan || !host_out) return THD_ERR_INVALID_ARG;
   if (!workspace) return THD_ERR_WORKSPACE;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (plan->kind) {  // one word per block of the launch
+    uint32_t part[256], all = 0;
+    for (int i = 0; i < plan->status_words; i += 256) {
+      const int n = plan->status_words - i < 256 ? plan->status_words - i : 256;
+      if (cudaMemcpyAsync(part, static_cast<const uint32_t*>(workspace) + i, 4 * n, cudaMemcpyDeviceToHost, stream) !=
+              cudaSuccess ||
+          cudaStreamSynchronize(stream) != cudaSuccess)
+        return THD_ERR_CUDA;
+      for (int j = 0; j < n; ++j) all |= part[j];
+    }
+    *host_out = all;
+    return THD_OK;
+  }
   const char* src = static_cast<const char*>(workspace) + plan->ws_off[0] + 4 * thd::kHdrStatus;
   uint32_t words[2] = {0u, 0u};
   if (cudaMemcpyAsync(&words[0], src, sizeof(uint32_t), cudaMemcpyDeviceToHost, stream) != cudaSuccess)

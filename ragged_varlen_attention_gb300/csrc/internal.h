@@ -249,7 +249,100 @@ constexpr int kBwdKeysPerUnit = 128;   // keys of a dK/dV unit
 cudaError_t launch_bwd_prep(const BwdParams& p, thd_dtype_t dtype, int num_sms, cudaStream_t stream);
 cudaError_t launch_bwd_simt(const BwdParams& p, thd_dtype_t dtype, int num_sms, cudaStream_t stream);
 
+// SM count of the current device (0: no device).
+int current_device_sms();
+
+// --- the operators beside attention: norm with rotation, page tables, paged decode.
+// Their launches have no setup kernel that could clear one status word first, so
+// block i of a launch writes word i of an array (and block 0 clears the words no
+// block owns); thd_attn_read_status ORs the array.
+constexpr int kMaxStatusWords = 2 * 1024;
+__device__ __forceinline__ void write_status(uint32_t* status, int words, uint32_t bits) {
+  status[blockIdx.x] = bits;
+  if (blockIdx.x == 0)
+    for (int i = gridDim.x; i < words; ++i) status[i] = 0;
+}
+
+struct NormRopeParams {
+  const void* in[4];        // Q, K, then V (paged) or dQ out, dK out (backward)
+  void* out[3];             // Q out, K out / K cache, V cache; backward: dQ, dK
+  const void* w[2];         // w_q, w_k; null = ones
+  const float* cos_sin;
+  const int32_t* positions;
+  const int32_t* slot_map;  // paged
+  float* part_dw;           // backward: [blocks][2][d] partial weight gradients
+  float* dw[2];
+  int64_t in_tok[4], in_head[4];
+  int64_t out_page[3], out_tok[3], out_head[3];
+  int32_t rows, h_q, h_kv, d, rot, interleaved, max_pos;
+  int32_t page_size;
+  int64_t num_slots;        // num_pages * page_size
+  float eps;
+  int32_t zero_skipped;
+  uint32_t* status;
+};
+constexpr int kNormRopeMaxBlocks = 8 * kMaxSmsForSizing;
+static_assert(kNormRopeMaxBlocks <= kMaxStatusWords, "status words");
+// `vec`: every view, weight and the table allow 4-element accesses and rot % 8 == d % 8 == 0
+cudaError_t launch_norm_rope(const NormRopeParams& p, thd_dtype_t dtype, thd_norm_rope_form_t form, bool vec,
+                             int num_sms, cudaStream_t stream);
+
+struct PagedTablesParams {
+  const int32_t* seq_lens;
+  const int32_t* cu_new;
+  const int32_t* free_pages;
+  const int32_t* free_span;
+  int32_t* block_table;
+  int32_t* slot_map;
+  int32_t* positions;
+  int32_t* seq_lens_out;
+  int32_t* free_begin_out;
+  int64_t table_stride;
+  int32_t batch, page_size, num_pages, max_pages, cap_rows, cap_free;
+  uint32_t* status;
+};
+constexpr int kPagedMaxBatch = 8192;
+constexpr int kPagedTablesMaxBlocks = kMaxStatusWords;
+constexpr int kPagedTablesRowsPerBlock = 1024;
+cudaError_t launch_paged_tables(const PagedTablesParams& p, cudaStream_t stream);
+
+// What the join kernel needs to know of CTA c of a decode launch: the segment its
+// range starts in, that segment's tiles, and how many of them lie before the range.
+struct DecodeRec {
+  int32_t b, seg, tiles, before;
+};
+struct DecodeParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* stats;             // may be null
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* window;    // may be null
+  int64_t q_tok, q_head, o_tok, o_head;
+  int64_t k_page, k_tok, k_head, v_page, v_tok, v_head;
+  int64_t table_stride, stats_tok, stats_head;
+  int32_t batch, h_q, h_kv, d, group;
+  int32_t page_size, num_pages, max_pages;
+  float scale_log2;
+  uint32_t* status;         // one word per CTA
+  DecodeRec* recs;          // [ctas]
+  int64_t* total;           // tiles of the launch, CTAs that share them
+  float* part_o;            // [2 ctas][heads of a segment][d padded] normalised partial O
+  float* part_lse;          // [2 ctas][heads of a segment] base-2 log-sum-exp
+};
+constexpr int kDecodeCtasPerSm = 2;
+constexpr int kDecodeKeysPerTile = 64;
+constexpr int kDecodeMaxCtas = kDecodeCtasPerSm * kMaxSmsForSizing;
+// query heads a segment holds (a kv head whose group is larger has several segments)
+constexpr int decode_seg_heads(int group, bool mma) { return !mma || group <= 8 ? 8 : group <= 16 ? 16 : 32; }
+constexpr int decode_pad_d(int d) { return d <= 64 ? 64 : 128; }
+cudaError_t launch_paged_decode(const DecodeParams& p, thd_dtype_t dtype, bool mma, int num_sms, cudaStream_t stream);
+
 }  // namespace thd
+
+enum { kPlanNormRope = 1, kPlanPagedTables = 2, kPlanPagedDecode = 3 };
 
 struct thd_attn_plan_s {
   thd_attn_desc_t desc;
@@ -278,6 +371,12 @@ struct thd_attn_plan_s {
   int32_t is_indexer;
   thd_indexer_desc_t idesc;
   int64_t score_row;        // floats per output row in the score scratch
+  // plans of the operators beside attention (0: an attention or indexer plan)
+  int32_t kind;
+  int32_t status_words;     // words of the status array at the start of their workspace
+  thd_norm_rope_desc_t ndesc;
+  thd_paged_tables_desc_t tdesc;
+  thd_paged_decode_desc_t ddesc;
   // optional attention-kernel timing (thd_attn_profile_enable)
   int32_t prof_slots;
   int32_t prof_count;

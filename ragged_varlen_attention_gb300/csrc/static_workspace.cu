@@ -64,7 +64,7 @@ thd_status_t thd_attn_fwd_static_ws(thd_attn_plan_t plan, const void* q, const v
                                     const int32_t* off_v, const int32_t* off_o, const int32_t* off_s,
                                     const int8_t* mask_type, const int32_t* q_causal_offset, void* stream) {
   // only forward plans run here, whatever their workspace size
-  if (!plan || plan->is_bwd || plan->is_indexer) return THD_ERR_INVALID_ARG;
+  if (!plan || plan->is_bwd || plan->is_indexer || plan->kind) return THD_ERR_INVALID_ARG;
   if (plan->ws_bytes > kStaticWorkspaceBytes) return THD_ERR_WORKSPACE;
   void* ws = nullptr;
   const thd_status_t st = static_address(&ws);
@@ -74,7 +74,7 @@ thd_status_t thd_attn_fwd_static_ws(thd_attn_plan_t plan, const void* q, const v
 }
 
 thd_status_t thd_attn_static_read_status(thd_attn_plan_t plan, uint32_t* host_out, void* stream) {
-  if (!plan || !host_out || plan->is_bwd || plan->is_indexer) return THD_ERR_INVALID_ARG;
+  if (!plan || !host_out || plan->is_bwd || plan->is_indexer || plan->kind) return THD_ERR_INVALID_ARG;
   void* ws = nullptr;
   const thd_status_t st = static_address(&ws);
   if (st != THD_OK) return st;
