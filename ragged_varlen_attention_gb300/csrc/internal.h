@@ -258,7 +258,14 @@ int current_device_sms();
 // block owns); thd_attn_read_status ORs the array.
 constexpr int kMaxStatusWords = 2 * 1024;
 __device__ __forceinline__ void write_status(uint32_t* status, int words, uint32_t bits) {
-  status[blockIdx.x] = bits;
+  __shared__ uint32_t all;  // the OR over the block's threads; every thread calls
+  if (threadIdx.x == 0) all = 0;
+  __syncthreads();
+  bits = __reduce_or_sync(0xffffffffu, bits);
+  if ((threadIdx.x & 31) == 0 && bits) atomicOr(&all, bits);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  status[blockIdx.x] = all;
   if (blockIdx.x == 0)
     for (int i = gridDim.x; i < words; ++i) status[i] = 0;
 }

@@ -267,8 +267,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeParams p) {
       p.part_dw[(int64_t)blockIdx.x * 2 * p.d + i] = v;
     }
   }
-  const uint32_t bits = __syncthreads_or((int)status);
-  if (threadIdx.x == 0) write_status(p.status, kNormRopeMaxBlocks, bits);
+  write_status(p.status, kNormRopeMaxBlocks, status);
 }
 
 // Any d <= 256, any rot, any strides: a warp per (row, head), elements strided over
@@ -389,8 +388,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeParams 
       p.part_dw[(int64_t)blockIdx.x * 2 * p.d + i] = s;
     }
   }
-  const uint32_t bits = __syncthreads_or((int)status);
-  if (threadIdx.x == 0) write_status(p.status, kNormRopeMaxBlocks, bits);
+  write_status(p.status, kNormRopeMaxBlocks, status);
 }
 
 // dw = sum over the blocks' partial rows, 32 columns to a block, in a fixed order.

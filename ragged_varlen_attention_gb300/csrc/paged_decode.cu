@@ -528,8 +528,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
     cur.advance(p, segs, step + 1 < steps);
   }
   cp_wait<0>();
-  const uint32_t bits = __syncthreads_or((int)status);
-  if (threadIdx.x == 0) write_status(p.status, kDecodeMaxCtas, bits);
+  write_status(p.status, kDecodeMaxCtas, status);
 }
 
 // --------------------------------------------------------------- SIMT kernel
@@ -666,8 +665,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParam
     }
     cur.advance(p, segs, step + 1 < steps);
   }
-  const uint32_t bits = __syncthreads_or((int)status);
-  if (threadIdx.x == 0) write_status(p.status, kDecodeMaxCtas, bits);
+  write_status(p.status, kDecodeMaxCtas, status);
 }
 
 // ----------------------------------------------------------------- join kernel

@@ -164,8 +164,7 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(PagedTablesParam
         p.positions[row0 + i] = position[i];
       }
   }
-  const uint32_t bits = __syncthreads_or((int)status);
-  if (threadIdx.x == 0) write_status(p.status, kPagedTablesMaxBlocks, bits);
+  write_status(p.status, kPagedTablesMaxBlocks, status);
 }
 
 }  // namespace
