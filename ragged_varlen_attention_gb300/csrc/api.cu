@@ -380,16 +380,13 @@ thd_status_t thd_attn_read_status(thd_attn_plan_t plan, const void* workspace, u
   if (!plan || !host_out) return THD_ERR_INVALID_ARG;
   if (!workspace) return THD_ERR_WORKSPACE;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  if (plan->kind) {  // one word per block of the launch
-    uint32_t part[256], all = 0;
-    for (int i = 0; i < plan->status_words; i += 256) {
-      const int n = plan->status_words - i < 256 ? plan->status_words - i : 256;
-      if (cudaMemcpyAsync(part, static_cast<const uint32_t*>(workspace) + i, 4 * n, cudaMemcpyDeviceToHost, stream) !=
-              cudaSuccess ||
-          cudaStreamSynchronize(stream) != cudaSuccess)
-        return THD_ERR_CUDA;
-      for (int j = 0; j < n; ++j) all |= part[j];
-    }
+  if (plan->kind) {  // the number of blocks, then a word of each
+    uint32_t words[1 + thd::kMaxStatusBlocks], all = 0;
+    if (cudaMemcpyAsync(words, workspace, 4 * (1 + plan->status_blocks), cudaMemcpyDeviceToHost, stream) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+      return THD_ERR_CUDA;
+    for (uint32_t i = 0; i < words[0] && i < (uint32_t)plan->status_blocks; ++i) all |= words[1 + i];
     *host_out = all;
     return THD_OK;
   }

@@ -254,10 +254,10 @@ int current_device_sms();
 
 // --- the operators beside attention: norm with rotation, page tables, paged decode.
 // Their launches have no setup kernel that could clear one status word first, so
-// block i of a launch writes word i of an array (and block 0 clears the words no
-// block owns); thd_attn_read_status ORs the array.
-constexpr int kMaxStatusWords = 2 * 1024;
-__device__ __forceinline__ void write_status(uint32_t* status, int words, uint32_t bits) {
+// block i of a launch writes word 1 + i of an array and block 0 the number of blocks
+// into word 0; thd_attn_read_status ORs the words that the last launch wrote.
+constexpr int kMaxStatusBlocks = 2 * 1024;
+__device__ __forceinline__ void write_status(uint32_t* status, uint32_t bits) {
   __shared__ uint32_t all;  // the OR over the block's threads; every thread calls
   if (threadIdx.x == 0) all = 0;
   __syncthreads();
@@ -265,9 +265,8 @@ __device__ __forceinline__ void write_status(uint32_t* status, int words, uint32
   if ((threadIdx.x & 31) == 0 && bits) atomicOr(&all, bits);
   __syncthreads();
   if (threadIdx.x != 0) return;
-  status[blockIdx.x] = all;
-  if (blockIdx.x == 0)
-    for (int i = gridDim.x; i < words; ++i) status[i] = 0;
+  status[1 + blockIdx.x] = all;
+  if (blockIdx.x == 0) status[0] = gridDim.x;
 }
 
 struct NormRopeParams {
@@ -289,7 +288,7 @@ struct NormRopeParams {
   uint32_t* status;
 };
 constexpr int kNormRopeMaxBlocks = 8 * kMaxSmsForSizing;
-static_assert(kNormRopeMaxBlocks <= kMaxStatusWords, "status words");
+static_assert(kNormRopeMaxBlocks <= kMaxStatusBlocks, "status words");
 // `vec`: every view, weight and the table allow 4-element accesses and rot % 8 == d % 8 == 0
 cudaError_t launch_norm_rope(const NormRopeParams& p, thd_dtype_t dtype, thd_norm_rope_form_t form, bool vec,
                              int num_sms, cudaStream_t stream);
@@ -309,14 +308,14 @@ struct PagedTablesParams {
   uint32_t* status;
 };
 constexpr int kPagedMaxBatch = 8192;
-constexpr int kPagedTablesMaxBlocks = kMaxStatusWords;
+constexpr int kPagedTablesMaxBlocks = kMaxStatusBlocks;
 constexpr int kPagedTablesRowsPerBlock = 1024;
 cudaError_t launch_paged_tables(const PagedTablesParams& p, cudaStream_t stream);
 
-// What the join kernel needs to know of CTA c of a decode launch: the segment its
-// range starts in, that segment's tiles, and how many of them lie before the range.
+// What the join kernel needs to know of worker (warp) w of a decode launch: the segment
+// its range starts in, that segment's chunks, and how many of them lie before the range.
 struct DecodeRec {
-  int32_t b, seg, tiles, before;
+  int32_t b, seg, chunks, before;
 };
 struct DecodeParams {
   const void* q;
@@ -333,15 +332,16 @@ struct DecodeParams {
   int32_t batch, h_q, h_kv, d, group;
   int32_t page_size, num_pages, max_pages;
   float scale_log2;
-  uint32_t* status;         // one word per CTA
-  DecodeRec* recs;          // [ctas]
-  int64_t* total;           // tiles of the launch, CTAs that share them
-  float* part_o;            // [2 ctas][heads of a segment][d padded] normalised partial O
-  float* part_lse;          // [2 ctas][heads of a segment] base-2 log-sum-exp
+  uint32_t* status;
+  DecodeRec* recs;          // [workers]
+  int64_t* total;           // chunks of the launch, workers that share them
+  float* part_o;            // [2 workers][heads of a segment][d padded] normalised partial O
+  float* part_lse;          // [2 workers][heads of a segment] base-2 log-sum-exp
 };
 constexpr int kDecodeCtasPerSm = 2;
-constexpr int kDecodeKeysPerTile = 64;
+constexpr int kDecodeMinChunk = 16;   // keys of the smallest unit of the schedule
 constexpr int kDecodeMaxCtas = kDecodeCtasPerSm * kMaxSmsForSizing;
+constexpr int kDecodeMaxWorkers = 4 * kDecodeMaxCtas;
 // query heads a segment holds (a kv head whose group is larger has several segments)
 constexpr int decode_seg_heads(int group, bool mma) { return !mma || group <= 8 ? 8 : group <= 16 ? 16 : 32; }
 constexpr int decode_pad_d(int d) { return d <= 64 ? 64 : 128; }
@@ -380,7 +380,7 @@ struct thd_attn_plan_s {
   int64_t score_row;        // floats per output row in the score scratch
   // plans of the operators beside attention (0: an attention or indexer plan)
   int32_t kind;
-  int32_t status_words;     // words of the status array at the start of their workspace
+  int32_t status_blocks;    // capacity in blocks of the status array at the start of their workspace
   thd_norm_rope_desc_t ndesc;
   thd_paged_tables_desc_t tdesc;
   thd_paged_decode_desc_t ddesc;

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeParams p) {
       p.part_dw[(int64_t)blockIdx.x * 2 * p.d + i] = v;
     }
   }
-  write_status(p.status, kNormRopeMaxBlocks, status);
+  write_status(p.status, status);
 }
 
 // Any d <= 256, any rot, any strides: a warp per (row, head), elements strided over
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeParams 
       p.part_dw[(int64_t)blockIdx.x * 2 * p.d + i] = s;
     }
   }
-  write_status(p.status, kNormRopeMaxBlocks, status);
+  write_status(p.status, status);
 }
 
 // dw = sum over the blocks' partial rows, 32 columns to a block, in a fixed order.

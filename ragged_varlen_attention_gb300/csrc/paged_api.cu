@@ -18,13 +18,13 @@ int elem_bytes(thd_dtype_t t) { return t == THD_FP32 ? 4 : 2; }
 bool known_dtype(thd_dtype_t t) { return t == THD_BF16 || t == THD_FP16 || t == THD_FP32; }
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-thd_attn_plan_s* new_plan(int kind, int status_words) {
+thd_attn_plan_s* new_plan(int kind, int status_blocks) {
   auto* p = new (std::nothrow) thd_attn_plan_s;
   if (!p) return nullptr;
   std::memset(p, 0, sizeof(*p));
   p->kind = kind;
   p->kernel = THD_KERNEL_SIMT;
-  p->status_words = status_words;
+  p->status_blocks = status_blocks;
   return p;
 }
 
@@ -81,7 +81,7 @@ thd_status_t thd_qk_norm_rope_plan(thd_attn_plan_t* out, const thd_norm_rope_des
   if (!p) return THD_ERR_INVALID_ARG;
   p->ndesc = d;
   p->elem_bytes = eb;
-  int64_t off = align_up(4 * thd::kNormRopeMaxBlocks);
+  int64_t off = align_up(4 * (1 + thd::kNormRopeMaxBlocks));
   p->ws_off[1] = off;
   if (d.form == THD_NORM_ROPE_BWD) off = align_up(off + (int64_t)thd::kNormRopeMaxBlocks * 2 * d.d * 4);
   p->ws_bytes = (size_t)off;
@@ -200,7 +200,7 @@ thd_status_t thd_paged_tables_plan(thd_attn_plan_t* out, const thd_paged_tables_
   auto* p = new_plan(kPlanPagedTables, thd::kPagedTablesMaxBlocks);
   if (!p) return THD_ERR_INVALID_ARG;
   p->tdesc = d;
-  p->ws_bytes = (size_t)align_up(4 * thd::kPagedTablesMaxBlocks);
+  p->ws_bytes = (size_t)align_up(4 * (1 + thd::kPagedTablesMaxBlocks));
   *ws_bytes = p->ws_bytes;
   *out = p;
   return THD_OK;
@@ -259,7 +259,8 @@ thd_status_t thd_paged_decode_plan(thd_attn_plan_t* out, const thd_paged_decode_
       return THD_ERR_INVALID_ARG;
     if (cache)
       mma = mma && d.stride_tok[i] * eb % 16 == 0 && d.stride_head[i] * eb % 16 == 0 && d.stride_page[i] * eb % 16 == 0;
-    if (i == 0) mma = mma && d.stride_tok[i] % 2 == 0 && d.stride_head[i] % 2 == 0;  // Q is read in pairs
+    else
+      mma = mma && d.stride_tok[i] % 2 == 0 && d.stride_head[i] % 2 == 0;  // Q and O are accessed in pairs
     if (d.bytes[i] == 0) continue;
     const int64_t span = cache ? cache_span(d.num_pages, d.page_size, heads[i], d.d, d.stride_page[i], d.stride_tok[i],
                                             d.stride_head[i], eb)
@@ -271,9 +272,9 @@ thd_status_t thd_paged_decode_plan(thd_attn_plan_t* out, const thd_paged_decode_
   const int group = d.h_q / d.h_kv;
   const int seg_heads = thd::decode_seg_heads(group, mma);
   const int64_t segs = (int64_t)d.h_kv * ((group + seg_heads - 1) / seg_heads);
-  const int64_t max_tiles = (int64_t)d.max_pages * d.page_size / thd::kDecodeKeysPerTile + 2;
-  // the line's tiles: below 2^31 for each CTA, and tiles x CTAs inside 64 bits
-  if ((double)d.batch * (double)segs * (double)max_tiles >= (double)(int64_t(1) << 37)) return THD_ERR_UNSUPPORTED;
+  const int64_t max_chunks = (int64_t)d.max_pages * d.page_size / thd::kDecodeMinChunk + 2;
+  // the line's chunks: below 2^31 for each worker, and chunks x workers inside 64 bits
+  if ((double)d.batch * (double)segs * (double)max_chunks >= (double)(int64_t(1) << 38)) return THD_ERR_UNSUPPORTED;
   auto* p = new_plan(kPlanPagedDecode, thd::kDecodeMaxCtas);
   if (!p) return THD_ERR_INVALID_ARG;
   p->ddesc = d;
@@ -281,12 +282,12 @@ thd_status_t thd_paged_decode_plan(thd_attn_plan_t* out, const thd_paged_decode_
   p->scale = scale;
   p->kernel = mma ? THD_KERNEL_MMA : THD_KERNEL_SIMT;
   p->rows_per_unit = seg_heads;
-  p->keys_per_tile = thd::kDecodeKeysPerTile;
+  p->keys_per_tile = thd::kDecodeMinChunk;
   p->stats_tok = d.stats_layout == THD_STATS_TOKEN_MAJOR ? d.h_q : 1;
   p->stats_head = d.stats_layout == THD_STATS_TOKEN_MAJOR ? 1 : d.batch;
-  const int64_t rows = 2 * (int64_t)thd::kDecodeMaxCtas * seg_heads;
-  int64_t off = align_up(4 * thd::kDecodeMaxCtas);
-  p->ws_off[1] = off; off = align_up(off + thd::kDecodeMaxCtas * (int64_t)sizeof(thd::DecodeRec));
+  const int64_t rows = 2 * (int64_t)thd::kDecodeMaxWorkers * seg_heads;
+  int64_t off = align_up(4 * (1 + thd::kDecodeMaxCtas));
+  p->ws_off[1] = off; off = align_up(off + thd::kDecodeMaxWorkers * (int64_t)sizeof(thd::DecodeRec));
   p->ws_off[2] = off; off = align_up(off + 2 * 8);
   p->ws_off[3] = off; off = align_up(off + rows * thd::decode_pad_d(d.d) * 4);
   p->ws_off[4] = off; off = align_up(off + rows * 4);
@@ -305,7 +306,7 @@ thd_status_t thd_paged_decode(thd_attn_plan_t plan, const void* q, const void* k
   if (d.batch > 0 && (!q || !o || !seq_lens)) return THD_ERR_INVALID_ARG;
   if (d.batch > 0 && d.max_pages > 0 && !block_table) return THD_ERR_INVALID_ARG;
   if (d.num_pages > 0 && (!k_cache || !v_cache)) return THD_ERR_INVALID_ARG;
-  if (plan->kernel == THD_KERNEL_MMA && (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 4)))
+  if (plan->kernel == THD_KERNEL_MMA && (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 4) || !aligned(o, 4)))
     return THD_ERR_ALIGNMENT;
   thd::DecodeParams dp;
   dp.q = q; dp.k = k_cache; dp.v = v_cache; dp.o = o; dp.stats = stats;

@@ -7,15 +7,14 @@
 // memory bounds the kernel. What matters is that every SM streams at its share of
 // the bandwidth until the end, whatever the lengths are:
 //   - A segment is (request, kv head, up to 8/16/32 query heads of its group). All
-//     segments' key tiles (64 keys) form one line, and CTA c of n takes the tiles
-//     [c W / n, (c + 1) W / n) of it, across segment borders. The border positions
-//     follow from the lengths on the device; no setup kernel, no work list.
-//   - Each warp streams its own 16 of a tile's 64 keys through its own ring of
-//     cp.async stages and keeps its own running maximum, sum and output; warps meet
-//     only at the end of a segment, where their four results are joined.
-//   - A segment that lies inside one CTA is finished there. One that crosses a border
-//     leaves normalised partial outputs in the workspace, and the join kernel merges
-//     them in CTA order (no atomics: equal inputs give equal bits).
+//     segments' key chunks (16 or 32 keys) form one line, and warp w of n takes the
+//     chunks [w W / n, (w + 1) W / n) of it, across segment borders. The border
+//     positions follow from the lengths on the device; no setup kernel, no work list.
+//   - A warp streams its chunks through its own ring of stages and keeps its own
+//     running maximum, sum and output: no warp waits for another one.
+//   - A segment that lies inside one warp's range is finished there. One that crosses a
+//     border leaves normalised partial outputs in the workspace, and the join kernel
+//     merges them in the line's order (no atomics: equal inputs give equal bits).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,10 +27,12 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kChunk = 16;                    // keys of a warp's stage
-constexpr int kTile = kChunk * kWarps;        // keys of a CTA's step
-static_assert(kTile == kDecodeKeysPerTile, "the plan's bound counts these tiles");
 constexpr float kLn2 = 0.69314718055994530942f;
+// keys of a chunk: half of the rows that a warp's stage holds (K and V) with d = 128, all
+// of them with d = 64, so that a stage is 8 KB either way
+constexpr int chunk_keys(int pad_d) { return pad_d == 128 ? 16 : 32; }
+static_assert(chunk_keys(128) >= kDecodeMinChunk, "the plan's bound counts these chunks");
+static_assert(kWarps * kDecodeMaxCtas == kDecodeMaxWorkers, "the workspace is sized for these workers");
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -51,11 +52,12 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 // ------------------------------------------------------------------ schedule
-// Visible keys [lo, n) of a request; `base` = lo rounded down to a chunk.
+// Visible keys [lo, n) of a request; `base` = lo rounded down to a multiple of 16.
 struct Span {
-  int32_t n, lo, base, tiles;
+  int32_t n, lo, base, chunks;
   bool bad;
 };
+template <int KC>
 __device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
   Span s;
   s.n = p.seq_lens[b];
@@ -63,34 +65,35 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
   if (s.bad) s.n = 0;
   const int w = p.window ? p.window[b] : -1;
   s.lo = w >= 0 && w < s.n - 1 ? s.n - 1 - w : 0;
-  s.base = s.lo & ~(kChunk - 1);
-  s.tiles = (s.n - s.base + kTile - 1) / kTile;
+  s.base = s.lo & ~15;
+  s.chunks = (s.n - s.base + KC - 1) / KC;
   return s;
 }
 
-// Position in the line of tiles: request b, segment seg of its `segs`, tile of the
-// segment; sp is the request's span.
+// Position in the line of chunks: request b, segment seg of its `segs`, chunk of the
+// segment; sp is the request's span. The warp's lanes hold the same cursor.
+template <int KC>
 struct Cursor {
-  int32_t b, seg, tile;
+  int32_t b, seg, chunk;
   Span sp;
   // the next request with keys (the caller knows that there is one)
   __device__ __forceinline__ void skip_empty(const DecodeParams& p) {
     const int lane = threadIdx.x & 31;
     while (b < p.batch) {
       const int mine = b + lane;
-      const bool some = mine < p.batch && span_of(p, mine).tiles > 0;
+      const bool some = mine < p.batch && span_of<KC>(p, mine).chunks > 0;
       const uint32_t any = __ballot_sync(0xffffffffu, some);
       if (any) {
         b += __ffs(any) - 1;
-        sp = span_of(p, b);
+        sp = span_of<KC>(p, b);
         return;
       }
       b += 32;
     }
   }
   __device__ __forceinline__ void advance(const DecodeParams& p, int segs, bool more) {
-    if (++tile < sp.tiles) return;
-    tile = 0;
+    if (++chunk < sp.chunks) return;
+    chunk = 0;
     if (++seg < segs) return;
     seg = 0;
     ++b;
@@ -98,27 +101,24 @@ struct Cursor {
   }
 };
 
-struct Range {
-  int64_t total, begin, end;
-  int32_t ctas;
-};
+// First chunk of worker (warp) w of n over a line of `total` chunks.
+__device__ __forceinline__ int64_t line_start(int64_t w, int64_t total, int32_t n) { return w * total / n; }
 
-// First tile of CTA c of n over a line of w tiles.
-__device__ __forceinline__ int64_t cta_start(int64_t c, int64_t w, int32_t n) { return c * w / n; }
-
-// The CTA's range and the cursor at its beginning. Every thread calls it.
-__device__ __forceinline__ Range locate(const DecodeParams& p, int segs, Cursor& cur, uint32_t& status) {
+// The number of chunks in the warp's range, and the cursor at its beginning. Every thread
+// calls it. Leaves the join kernel's record of each worker.
+template <int KC>
+__device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC>& cur, uint32_t& status) {
   __shared__ int64_t warp_sums[kWarps];
-  __shared__ int32_t found_b;
-  __shared__ int64_t found_before;
+  __shared__ int32_t found_b[kWarps];
+  __shared__ int64_t found_before[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int strip = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.batch, (int)threadIdx.x * strip), b1 = min(p.batch, b0 + strip);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const Span s = span_of(p, b);
+    const Span s = span_of<KC>(p, b);
     if (s.bad) status |= THD_DEV_BAD_LENGTH;
-    mine += s.tiles;
+    mine += s.chunks;
   }
   int64_t upto = mine;
 #pragma unroll
@@ -128,48 +128,57 @@ __device__ __forceinline__ Range locate(const DecodeParams& p, int segs, Cursor&
   }
   if (lane == 31) warp_sums[warp] = upto;
   __syncthreads();
-  Range r;
-  r.total = 0;
+  int64_t total = 0;
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) upto += warp_sums[w];
-    r.total += warp_sums[w];
+    total += warp_sums[w];
   }
-  r.total *= segs;
-  r.ctas = (int32_t)min64(gridDim.x, max64(r.total, 1));
-  r.begin = r.end = 0;
-  if ((int)blockIdx.x < r.ctas) {
-    r.begin = cta_start(blockIdx.x, r.total, r.ctas);
-    r.end = cta_start(blockIdx.x + 1, r.total, r.ctas);
-  }
-  if (r.begin < r.end) {
+  total *= segs;
+  const int32_t workers = (int32_t)min64((int64_t)gridDim.x * kWarps, max64(total, 1));
+  // the request that each of the block's workers begins in
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t at = line_start((int64_t)blockIdx.x * kWarps + w, total, workers);
     int64_t before = (upto - mine) * segs;
-    if (before <= r.begin && r.begin < upto * segs) {
+    if (before <= at && at < upto * segs) {
       for (int b = b0; b < b1; ++b) {
-        const int64_t n = (int64_t)span_of(p, b).tiles * segs;
-        if (r.begin < before + n) {
-          found_b = b;
-          found_before = before;
+        const int64_t n = (int64_t)span_of<KC>(p, b).chunks * segs;
+        if (at < before + n) {
+          found_b[w] = b;
+          found_before[w] = before;
           break;
         }
         before += n;
       }
     }
-    __syncthreads();
-    cur.b = found_b;
-    cur.sp = span_of(p, cur.b);
-    const int64_t rel = r.begin - found_before;
-    cur.seg = (int)(rel / cur.sp.tiles);
-    cur.tile = (int)(rel - (int64_t)cur.seg * cur.sp.tiles);
   }
-  return r;
+  __syncthreads();
+  const int32_t worker = blockIdx.x * kWarps + warp;
+  DecodeRec rec = {0, 0, 0, 0};
+  int steps = 0;
+  if (worker < workers && total > 0) {
+    const int64_t begin = line_start(worker, total, workers);
+    steps = (int)(line_start(worker + 1, total, workers) - begin);  // below 2^31 by the plan's bound
+    cur.b = found_b[warp];
+    cur.sp = span_of<KC>(p, cur.b);
+    const int64_t rel = begin - found_before[warp];
+    cur.seg = (int)(rel / cur.sp.chunks);
+    cur.chunk = (int)(rel - (int64_t)cur.seg * cur.sp.chunks);
+    rec = {cur.b, cur.seg, cur.sp.chunks, cur.chunk};
+  }
+  if (lane == 0) p.recs[worker] = rec;
+  if (worker == 0 && lane == 0) {
+    p.total[0] = total;
+    p.total[1] = workers;
+  }
+  return steps;
 }
 
 // Rows without a visible key: O = 0, LSE = -inf.
 template <typename T>
 __device__ __forceinline__ void write_empty(const DecodeParams& p) {
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    const Span s = span_of(p, b);
-    if (s.bad || s.tiles > 0) continue;
+    const Span s = span_of<16>(p, b);
+    if (s.bad || s.chunks > 0) continue;
     for (int i = threadIdx.x; i < p.h_q * p.d; i += kThreads) {
       const int h = i / p.d, e = i - h * p.d;
       static_cast<T*>(p.o)[(int64_t)b * p.o_tok + (int64_t)h * p.o_head + e] = from_f<T>(0.f);
@@ -187,72 +196,13 @@ __device__ __forceinline__ int segment_heads(const DecodeParams& p, int seg, int
   return min(HEADS, p.group - c * HEADS);
 }
 
-// Joins the four warps' results for 8 heads of a segment (`h8` the first of them) and
-// writes the rows, or the partial rows when the segment goes on in another CTA.
-// part_max / part_sum / part_o hold each warp's base-2 maximum, sum and output.
-template <typename T, int D, int HEADS>
-__device__ __forceinline__ void join_warps(const DecodeParams& p, const float (&part_max)[kWarps][8],
-                                           const float (&part_sum)[kWarps][8],
-                                           const float (&part_o)[kWarps][8][D + 4], int b, int head0, int heads,
-                                           int h8, int slot) {
-  for (int i = threadIdx.x; i < 8 * (D / 4); i += kThreads) {
-    const int h = i / (D / 4), e = (i - h * (D / 4)) * 4;
-    float top = part_max[0][h];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, part_max[w][h]);
-    const bool dead = top == -INFINITY;
-    float sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!dead) {
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(part_max[w][h] - top);
-        const float4 a = *reinterpret_cast<const float4*>(&part_o[w][h][e]);
-        sum += f * part_sum[w][h];
-        o.x += f * a.x; o.y += f * a.y; o.z += f * a.z; o.w += f * a.w;
-      }
-    }
-    const float inv = dead ? 0.f : 1.f / sum;
-    o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-    const float lse2 = dead ? -INFINITY : top + log2f(sum);
-    if (slot >= 0) {
-      const int64_t row = (int64_t)slot * HEADS + h8 + h;
-      *reinterpret_cast<float4*>(p.part_o + row * D + e) = o;
-      if (e == 0) p.part_lse[row] = lse2;
-    } else if (h8 + h < heads) {
-      T* dst = static_cast<T*>(p.o) + (int64_t)b * p.o_tok + (int64_t)(head0 + h8 + h) * p.o_head;
-      const float v[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (e + k < p.d) dst[e + k] = from_f<T>(v[k]);
-      if (e == 0 && p.stats)
-        p.stats[(int64_t)b * p.stats_tok + (int64_t)(head0 + h8 + h) * p.stats_head] = dead ? -INFINITY : lse2 * kLn2;
-    }
-  }
-}
-
-// What the CTA records for the join kernel.
-__device__ __forceinline__ void write_record(const DecodeParams& p, const Range& range, const Cursor& cur) {
-  if (threadIdx.x != 0) return;
-  if (blockIdx.x == 0) {
-    p.total[0] = range.total;
-    p.total[1] = range.ctas;
-  }
-  DecodeRec rec = {0, 0, 0, 0};
-  if (range.begin < range.end) rec = {cur.b, cur.seg, cur.sp.tiles, cur.tile};
-  p.recs[blockIdx.x] = rec;
+// Where a worker leaves its piece of a segment: -1 when it holds the whole segment, 2w when
+// the segment began before worker w's range, 2w + 1 when it begins there and goes on.
+__device__ __forceinline__ int piece_slot(int worker, int first, int last, int chunks) {
+  return first > 0 ? 2 * worker : last + 1 < chunks ? 2 * worker + 1 : -1;
 }
 
 // ------------------------------------------------------------- matrix pieces
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  const int bytes = real ? 16 : 0;  // 0: the 16 bytes are zeros, src is not read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -304,55 +254,79 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 }
 
 // ------------------------------------------------- matrix-instruction kernel
-// A stage's 16 keys are the 16 rows of the instruction and the query heads its 8
-// columns: S^T = K Q^T, then O^T += V^T P^T, so a group of 8 heads fills the tile (the
-// other way round heads would be padded to 16). P^T's fragment is S^T's, transposed 8 x 8
-// by movmatrix; P is rounded to the storage type for the product (at most half a step
-// of a value <= 1), its sum is kept in float32.
+// 16 keys are the rows of the instruction and the query heads its 8 columns: S^T = K Q^T,
+// then O^T += V^T P^T, so a group of 8 heads fills the tile (the other way round heads
+// would be padded to 16). P^T's fragment is S^T's, transposed 8 x 8 by movmatrix; P is
+// rounded to the storage type for the product (at most half a step of a value <= 1),
+// its sum is kept in float32.
+//
+// Each lane copies whole rows of one key by bulk copies (K and V of key `lane`; with 16
+// keys a chunk, K by the lower lanes and V by the upper ones), so a page number is used by
+// the lane that looked it up and any page size or stride costs the same. Rows sit 16 bytes
+// apart from a multiple of 128, so that ldmatrix's eight rows fall into different banks
+// without a swizzle, and every address in the loop is a constant away from the stage's.
 template <int D>
 struct MmaSmem {
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kRowBytes = 2 * D;
-  static constexpr int kStageBytes = 2 * kChunk * kRowBytes;  // K rows, then V rows
+  static constexpr int kKeys = chunk_keys(D);
+  static constexpr int kStages = 3;
+  static constexpr int kPitch = 2 * D + 16;
+  static constexpr int kStageBytes = 2 * kKeys * kPitch;  // K rows, then V rows
   unsigned char ring[kWarps][kStages][kStageBytes];
-  float part_o[kWarps][8][D + 4];
-  float part_max[kWarps][8], part_sum[kWarps][8];
+  uint64_t full[kWarps][kStages];
   uint32_t seen[kWarps][kStages];  // bit r: key r of the stage is visible
 };
+
+// Waits for a phase of a barrier for at most about 2 s (a copy takes microseconds); false
+// when it gave up.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, parity))
+    if (ptx::globaltimer_ns() - t0 > 2000000000ull) return false;
+  return true;
+}
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_kernel(DecodeParams p) {
   using Smem = MmaSmem<D>;
   constexpr int kStages = Smem::kStages;
+  constexpr int kKeys = Smem::kKeys;
+  constexpr int MT = kKeys / 16;          // 16-key rows of the instruction in a chunk
   constexpr int kHeads = 8 * NT;
-  constexpr int kRowBytes = Smem::kRowBytes;
-  constexpr int kVecs = D / 8;            // 16-byte pieces of a row
-  constexpr int kRowsAtOnce = 32 / kVecs; // rows one warp-wide cp.async covers
+  constexpr int kPitch = Smem::kPitch;
   extern __shared__ __align__(128) unsigned char raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int worker = blockIdx.x * kWarps + warp;
   const int per = (p.group + kHeads - 1) / kHeads;   // segments of a kv head
   const int segs = p.h_kv * per;
   uint32_t status = 0;
-  Cursor cur;
-  const Range range = locate(p, segs, cur, status);
-  write_record(p, range, cur);
+  const uint32_t ring = ptx::smem_u32(sm.ring[warp]), full = ptx::smem_u32(sm.full[warp]);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) ptx::mbar_init(full + 8 * i, 1);
+    ptx::fence_mbar_init();
+  }
+  if (p.d < D) {  // the columns that no row copy fills are zeros throughout
+    for (int i = lane; i < (int)sizeof(sm.ring[0]) / 16; i += 32)
+      reinterpret_cast<uint4*>(sm.ring[warp])[i] = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+  }
+  Cursor<kKeys> cur;
+  int steps = locate<kKeys>(p, segs, cur, status);
   write_empty<T>(p);
 
-  const int steps = (int)(range.end - range.begin);  // below 2^31 by the plan's bound
-  Cursor load = cur;
+  Cursor<kKeys> load = cur;
   int issued = 0;
-  // the page of key `lane` of the warp's chunk at `load` (-1: none), looked up one step
+  uint32_t load_stage = 0;
+  // the page of key lane % kKeys of the chunk at `load` (-1: none), looked up one step
   // before it is used
-  const int vec = lane % kVecs, row_in = lane / kVecs;
-  const bool vec_real = vec * 8 < p.d;
   int key_page = -1, key_row = 0;
   auto look_up = [&]() {
     key_page = -1;
     if (issued >= steps) return;
-    const int key = load.sp.base + load.tile * kTile + warp * kChunk + (lane & (kChunk - 1));
+    const int key = load.sp.base + load.chunk * kKeys + (lane & (kKeys - 1));
     if (key >= load.sp.lo && key < load.sp.n) {
-      const int column = key / p.page_size;
+      const int column = (int)((uint32_t)key / (uint32_t)p.page_size);
       key_row = key - column * p.page_size;
       key_page = p.block_table[(int64_t)load.b * p.table_stride + column];
       if (key_page < 0 || key_page >= p.num_pages) {
@@ -361,49 +335,47 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
       }
     }
   };
+  const uint32_t row_bytes = 2 * p.d;
   auto issue = [&]() {
-    if (issued < steps) {
-      const int stage = issued % kStages;
-      const uint32_t seen = __ballot_sync(0xffffffffu, key_page >= 0) & 0xffffu;
-      if (lane == 0) sm.seen[warp][stage] = seen;
-      const uint32_t dst = ptx::smem_u32(sm.ring[warp][stage]);
-      const int g = load.seg / per;
-      const T* kh = static_cast<const T*>(p.k) + (int64_t)g * p.k_head + vec * 8;
-      const T* vh = static_cast<const T*>(p.v) + (int64_t)g * p.v_head + vec * 8;
-#pragma unroll
-      for (int i = 0; i < kChunk / kRowsAtOnce; ++i) {
-        const int row = i * kRowsAtOnce + row_in;
-        const int page = __shfl_sync(0xffffffffu, key_page, row);
-        const int in_page = __shfl_sync(0xffffffffu, key_row, row);
-        const bool real = page >= 0 && vec_real;
-        const uint32_t at = dst + row * kRowBytes + ((vec ^ (row & 7)) << 4);
-        const T* ks = static_cast<const T*>(p.k);
-        const T* vs = static_cast<const T*>(p.v);
-        if (real) {
-          ks = kh + (int64_t)page * p.k_page + (int64_t)in_page * p.k_tok;
-          vs = vh + (int64_t)page * p.v_page + (int64_t)in_page * p.v_tok;
-        }
-        cp_async16(at, ks, real);
-        cp_async16(at + kChunk * kRowBytes, vs, real);
-      }
-      ++issued;
-      load.advance(p, segs, issued < steps);
-      look_up();
+    if (issued >= steps) return;
+    const uint32_t seen = __ballot_sync(0xffffffffu, key_page >= 0) & (kKeys == 16 ? 0xffffu : 0xffffffffu);
+    const uint32_t bar = full + 8 * load_stage;
+    if (lane == 0) {
+      sm.seen[warp][load_stage] = seen;
+      ptx::mbar_arrive_expect_tx(bar, 2 * __popc(seen) * row_bytes);
     }
-    cp_commit();  // an empty group when there is nothing left: the count stays one per step
+    __syncwarp();
+    if (key_page >= 0) {
+      const int g = load.seg / per;
+      const uint32_t dst = ring + load_stage * Smem::kStageBytes + lane * kPitch;
+      const T* ks = static_cast<const T*>(p.k) + (int64_t)key_page * p.k_page + (int64_t)key_row * p.k_tok + (int64_t)g * p.k_head;
+      const T* vs = static_cast<const T*>(p.v) + (int64_t)key_page * p.v_page + (int64_t)key_row * p.v_tok + (int64_t)g * p.v_head;
+      if (kKeys == 16) {
+        ptx::bulk_load(dst, lane < 16 ? ks : vs, row_bytes, bar);
+      } else {
+        ptx::bulk_load(dst, ks, row_bytes, bar);
+        ptx::bulk_load(dst + kKeys * kPitch, vs, row_bytes, bar);
+      }
+    }
+    ++issued;
+    load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
+    load.advance(p, segs, issued < steps);
+    look_up();
   };
+  __syncwarp();
   look_up();
   for (int i = 0; i < kStages - 1; ++i) issue();
 
   uint32_t qf[D / 16][NT][2];
   float acc[D / 16][NT][4];
   float top[NT][2], sum[NT][2];
-  int head0 = 0, heads = 0, first_tile = 0;
+  int head0 = 0, heads = 0, first = 0;
   bool fresh = true;
+  uint32_t stage = 0, parity = 0;
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
-      first_tile = cur.tile;
+      first = cur.chunk;
       heads = segment_heads<kHeads>(p, cur.seg, head0);
       const T* q = static_cast<const T*>(p.q) + (int64_t)cur.b * p.q_tok;
 #pragma unroll
@@ -425,51 +397,85 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
           for (int j = 0; j < 4; ++j) acc[dt][nt][j] = 0.f;
       }
     }
-    cp_wait<kStages - 2>();
-    __syncwarp();
-    const int stage = step % kStages;
+    if (!wait_phase(full + 8 * stage, parity)) {
+      status |= THD_DEV_WAIT_TIMEOUT;
+      steps = issued;  // no further copies; those in flight are waited for (with the same limit)
+    }
     const uint32_t seen = sm.seen[warp][stage];
+    const uint32_t kbase = ring + stage * Smem::kStageBytes;
+    const uint32_t vbase = kbase + kKeys * kPitch;
+    if (seen != (kKeys == 16 ? 0xffffu : 0xffffffffu)) {
+      // V rows that were not copied hold anything: 0 x NaN must not reach the sums
+      for (int r = 0; r < kKeys; ++r)
+        if (!((seen >> r) & 1) && lane < D / 8)
+          *reinterpret_cast<uint4*>(sm.ring[warp][stage] + (kKeys + r) * kPitch + lane * 16) = make_uint4(0u, 0u, 0u, 0u);
+      ptx::fence_proxy_async_smem();  // before the next copy into these rows
+      __syncwarp();
+    }
     if (seen != 0) {
-      const uint32_t kbase = ptx::smem_u32(sm.ring[warp][stage]);
-      const uint32_t vbase = kbase + kChunk * kRowBytes;
-      float s[NT][4];
+      float s[MT][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-      {
-        const int row = lane & 15, half = lane >> 4;
+      for (int mt = 0; mt < MT; ++mt) {
+        float odd[NT][4];  // two chains of products, half as long each
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][nt][j] = odd[nt][j] = 0.f;
+        // matrices in order: keys 0-7 / d 0-7, keys 8-15 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 8-15
+        const uint32_t at = kbase + (mt * 16 + (lane & 15)) * kPitch + (lane >> 4) * 16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           uint32_t a[4];
-          ldsm4(a, kbase + row * kRowBytes + (((kk * 2 + half) ^ (row & 7)) << 4));
+          ldsm4(a, at + kk * 32);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<T>(s[nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+          for (int nt = 0; nt < NT; ++nt) mma16816<T>(kk & 1 ? odd[nt] : s[mt][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][nt][j] += odd[nt][j];
       }
-      const bool see0 = (seen >> (lane / 4)) & 1, see1 = (seen >> (lane / 4 + 8)) & 1;
-      uint32_t pb[NT][2];
+      uint32_t pb[MT][NT][2];
       float scale[NT][2];
       bool moved = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          s[nt][j] = see0 ? s[nt][j] * p.scale_log2 : -INFINITY;
-          s[nt][j + 2] = see1 ? s[nt][j + 2] * p.scale_log2 : -INFINITY;
-          float m = fmaxf(s[nt][j], s[nt][j + 2]);
+          float m = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const bool see = (seen >> (mt * 16 + half * 8 + lane / 4)) & 1;
+              float& v = s[mt][nt][j + 2 * half];
+              v = see ? v * p.scale_log2 : -INFINITY;
+              m = fmaxf(m, v);
+            }
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
           m = fmaxf(m, top[nt][j]);
           const float ref = m == -INFINITY ? 0.f : m;
-          scale[nt][j] = exp2f(top[nt][j] - ref);
+          scale[nt][j] = ptx::ex2(top[nt][j] - ref);
           moved |= m != top[nt][j];
           top[nt][j] = m;
-          s[nt][j] = exp2f(s[nt][j] - ref);
-          s[nt][j + 2] = exp2f(s[nt][j + 2] - ref);
-          sum[nt][j] = sum[nt][j] * scale[nt][j] + (s[nt][j] + s[nt][j + 2]);
+          float add = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float& v = s[mt][nt][j + 2 * half];
+              v = ptx::ex2(v - ref);
+              add += v;
+            }
+          sum[nt][j] = sum[nt][j] * scale[nt][j] + add;
         }
-        pb[nt][0] = transpose8x8(pack2<T>(s[nt][0], s[nt][1]));
-        pb[nt][1] = transpose8x8(pack2<T>(s[nt][2], s[nt][3]));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          pb[mt][nt][0] = transpose8x8(pack2<T>(s[mt][nt][0], s[mt][nt][1]));
+          pb[mt][nt][1] = transpose8x8(pack2<T>(s[mt][nt][2], s[mt][nt][3]));
+        }
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -479,85 +485,100 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[dt][nt][j] *= scale[nt][j & 1];
       }
-      {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
         // matrices in order: keys 0-7 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 0-7, keys 8-15 / d 8-15
-        const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+        const uint32_t at = vbase + (mt * 16 + (lane & 7) + ((lane >> 4) << 3)) * kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) {
           uint32_t a[4];
-          ldsm4_t(a, vbase + row * kRowBytes + (((dt * 2 + half) ^ (row & 7)) << 4));
+          ldsm4_t(a, at + dt * 32);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<T>(acc[dt][nt], a, pb[nt][0], pb[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) mma16816<T>(acc[dt][nt], a, pb[mt][nt][0], pb[mt][nt][1]);
         }
       }
     }
     __syncwarp();  // the stage is read by every lane before it is filled again
     issue();
+    if (++stage == kStages) {
+      stage = 0;
+      parity ^= 1;
+    }
 
-    const bool last = cur.tile + 1 == cur.sp.tiles || step + 1 == steps;
-    if (last) {
-      // -1: the CTA holds the whole segment; 2c: it began before CTA c; 2c + 1: it goes on behind it
-      const int slot =
-          first_tile > 0 ? 2 * (int)blockIdx.x : cur.tile + 1 < cur.sp.tiles ? 2 * (int)blockIdx.x + 1 : -1;
+    if (cur.chunk + 1 == cur.sp.chunks || step + 1 == steps) {
+      const int slot = piece_slot(worker, first, cur.chunk, cur.sp.chunks);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (nt * 8 >= heads) break;
+        float inv[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float l = sum[nt][j];
           l += __shfl_xor_sync(0xffffffffu, l, 4);
           l += __shfl_xor_sync(0xffffffffu, l, 8);
           l += __shfl_xor_sync(0xffffffffu, l, 16);
-          const int h = (lane % 4) * 2 + j;
+          const int h = nt * 8 + (lane % 4) * 2 + j;
+          const bool dead = top[nt][j] == -INFINITY;
+          inv[j] = dead ? 0.f : 1.f / l;
+          const float lse2 = dead ? -INFINITY : top[nt][j] + log2f(l);
           if (lane < 4) {
-            sm.part_max[warp][h] = top[nt][j];
-            sm.part_sum[warp][h] = l;
-          }
-#pragma unroll
-          for (int dt = 0; dt < D / 16; ++dt) {
-            sm.part_o[warp][h][dt * 16 + lane / 4] = acc[dt][nt][j];
-            sm.part_o[warp][h][dt * 16 + lane / 4 + 8] = acc[dt][nt][j + 2];
+            if (slot >= 0) p.part_lse[(int64_t)slot * kHeads + h] = lse2;
+            else if (h < heads && p.stats)
+              p.stats[(int64_t)cur.b * p.stats_tok + (int64_t)(head0 + h) * p.stats_head] = lse2 * kLn2;
           }
         }
-        __syncthreads();
-        join_warps<T, D, kHeads>(p, sm.part_max, sm.part_sum, sm.part_o, cur.b, head0, heads, nt * 8, slot);
-        __syncthreads();
+        if (slot >= 0) {
+          // 8 lanes write 32 consecutive bytes of a head's row
+          float* row = p.part_o + ((int64_t)slot * kHeads + nt * 8 + (lane % 4) * 2) * D + lane / 4;
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) row[(j & 1) * D + dt * 16 + (j >> 1) * 8] = acc[dt][nt][j] * inv[j & 1];
+        } else {
+          const int h = nt * 8 + lane / 4;
+          T* row = static_cast<T*>(p.o) + (int64_t)cur.b * p.o_tok + (int64_t)(head0 + h) * p.o_head;
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t v = transpose8x8(pack2<T>(acc[dt][nt][2 * half] * inv[0], acc[dt][nt][2 * half + 1] * inv[1]));
+              const int e = dt * 16 + half * 8 + (lane % 4) * 2;
+              if (h < heads && e < p.d) *reinterpret_cast<uint32_t*>(row + e) = v;
+            }
+        }
       }
       fresh = true;
     }
     cur.advance(p, segs, step + 1 < steps);
   }
-  cp_wait<0>();
-  write_status(p.status, kDecodeMaxCtas, status);
+  write_status(p.status, status);
 }
 
 // --------------------------------------------------------------- SIMT kernel
-// float32 caches, and any d <= 128 and alignment: the same schedule and join, each warp's
-// 16 keys taken 4 at a time with the head's elements spread over the lanes.
+// float32 caches, and any d <= 128 and alignment: the same schedule, a warp's 16 keys
+// taken 4 at a time with the head's elements spread over the lanes.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParams p) {
   constexpr int kHeads = 8;
   constexpr int kPer = D / 32;  // elements of a lane: e = lane + 32 i
+  constexpr int kChunk = 16;
   constexpr int kKeys = 4;
-  __shared__ __align__(16) float part_o[kWarps][8][D + 4];
-  __shared__ float part_max[kWarps][8], part_sum[kWarps][8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int lane = threadIdx.x & 31;
+  const int worker = blockIdx.x * kWarps + threadIdx.x / 32;
   const int per = (p.group + kHeads - 1) / kHeads;
   const int segs = p.h_kv * per;
   uint32_t status = 0;
-  Cursor cur;
-  const Range range = locate(p, segs, cur, status);
-  write_record(p, range, cur);
+  Cursor<kChunk> cur;
+  const int steps = locate<kChunk>(p, segs, cur, status);
   write_empty<T>(p);
 
-  const int steps = (int)(range.end - range.begin);  // below 2^31 by the plan's bound
   float q[8][kPer], acc[8][kPer], top[8], sum[8];
-  int head0 = 0, heads = 0, first_tile = 0;
+  int head0 = 0, heads = 0, first = 0;
   bool fresh = true;
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
-      first_tile = cur.tile;
+      first = cur.chunk;
       heads = segment_heads<kHeads>(p, cur.seg, head0);
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
@@ -576,9 +597,9 @@ __global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParam
     const T* vh = static_cast<const T*>(p.v) + (int64_t)g * p.v_head;
     int page = -1, in_page = 0;
     {
-      const int key = cur.sp.base + cur.tile * kTile + warp * kChunk + (lane & (kChunk - 1));
+      const int key = cur.sp.base + cur.chunk * kChunk + (lane & (kChunk - 1));
       if (key >= cur.sp.lo && key < cur.sp.n) {
-        const int column = key / p.page_size;
+        const int column = (int)((uint32_t)key / (uint32_t)p.page_size);
         in_page = key - column * p.page_size;
         page = p.block_table[(int64_t)cur.b * p.table_stride + column];
         if (page < 0 || page >= p.num_pages) {
@@ -646,98 +667,122 @@ __global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParam
         }
       }
     }
-    if (cur.tile + 1 == cur.sp.tiles || step + 1 == steps) {
-      const int slot =
-          first_tile > 0 ? 2 * (int)blockIdx.x : cur.tile + 1 < cur.sp.tiles ? 2 * (int)blockIdx.x + 1 : -1;
+    if (cur.chunk + 1 == cur.sp.chunks || step + 1 == steps) {
+      const int slot = piece_slot(worker, first, cur.chunk, cur.sp.chunks);
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
-        if (lane == 0) {
-          part_max[warp][h] = top[h];
-          part_sum[warp][h] = sum[h];
-        }
+        if (h >= heads) break;
+        const bool dead = top[h] == -INFINITY;
+        const float inv = dead ? 0.f : 1.f / sum[h];
+        const float lse2 = dead ? -INFINITY : top[h] + log2f(sum[h]);
+        T* row = static_cast<T*>(p.o) + (int64_t)cur.b * p.o_tok + (int64_t)(head0 + h) * p.o_head;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) part_o[warp][h][lane + 32 * i] = acc[h][i];
+        for (int i = 0; i < kPer; ++i) {
+          const int e = lane + 32 * i;
+          if (slot >= 0) p.part_o[((int64_t)slot * kHeads + h) * D + e] = acc[h][i] * inv;
+          else if (e < p.d) row[e] = from_f<T>(acc[h][i] * inv);
+        }
+        if (lane == 0) {
+          if (slot >= 0) p.part_lse[(int64_t)slot * kHeads + h] = lse2;
+          else if (p.stats) p.stats[(int64_t)cur.b * p.stats_tok + (int64_t)(head0 + h) * p.stats_head] = lse2 * kLn2;
+        }
       }
-      __syncthreads();
-      join_warps<T, D, kHeads>(p, part_max, part_sum, part_o, cur.b, head0, heads, 0, slot);
-      __syncthreads();
       fresh = true;
     }
     cur.advance(p, segs, step + 1 < steps);
   }
-  write_status(p.status, kDecodeMaxCtas, status);
+  write_status(p.status, status);
 }
 
 // ----------------------------------------------------------------- join kernel
-// Block (c, h): if CTA c's range is the first to begin inside a segment, merge the
-// segment's pieces for its head h. The piece that begins the segment is slot
-// 2 (c - 1) + 1, the others are slots 2c, 2 (c + 1), ... The four warps take the
-// pieces in turn, then their results are merged in warp order.
+// Block (w, t): if worker w's range is the first to begin inside a segment, merge the
+// segment's pieces for 8 of its heads. The piece that begins the segment is slot
+// 2 (w - 1) + 1, the others are slots 2w, 2 (w + 1), ... Each warp takes every eighth piece
+// with all 8 heads (4 KB in flight at d = 128), then the warps' results are merged in order.
+constexpr int kJoinWarps = 8;
 template <typename T, int D, int HEADS>
-__global__ void __launch_bounds__(kThreads) paged_decode_join_kernel(DecodeParams p) {
-  __shared__ __align__(16) float part_o[kWarps][D];
-  __shared__ float part_max[kWarps], part_sum[kWarps];
-  const int64_t total = p.total[0];
-  const int32_t ctas = (int32_t)p.total[1];
-  const int c = blockIdx.x;
-  if (c == 0 || c >= ctas || total == 0) return;
-  const DecodeRec rec = p.recs[c];
-  if (rec.before == 0) return;
-  int head0;
-  const int heads = segment_heads<HEADS>(p, rec.seg, head0);
-  const int h = blockIdx.y;
-  if (h >= heads) return;
-  const int64_t begin = cta_start(c, total, ctas) - rec.before, end = begin + rec.tiles;
-  if (cta_start(c - 1, total, ctas) > begin) return;  // an earlier block's
-  // the CTA that holds the segment's last tile
-  const int c_last = (int)((end * ctas - 1) / total);
-  const int pieces = c_last - c + 2;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_decode_join_kernel(DecodeParams p) {
   constexpr int kPer = D / 32;
-  float top = -INFINITY, sum = 0.f, acc[kPer];
+  __shared__ float part_o[kJoinWarps][8][D];
+  __shared__ float part_max[kJoinWarps][8], part_sum[kJoinWarps][8];
+  const int64_t total = p.total[0];
+  const int32_t workers = (int32_t)p.total[1];
+  const int w0 = blockIdx.x;
+  if (w0 == 0 || w0 >= workers || total == 0) return;
+  const DecodeRec rec = p.recs[w0];
+  if (rec.before == 0) return;
+  const int64_t begin = line_start(w0, total, workers) - rec.before, end = begin + rec.chunks;
+  if (line_start(w0 - 1, total, workers) > begin) return;  // an earlier block's
+  int head0;
+  const int h8 = blockIdx.y * 8;
+  const int heads = segment_heads<HEADS>(p, rec.seg, head0) - h8;
+  if (heads <= 0) return;
+  // the worker that holds the segment's last chunk
+  const int w_last = (int)((end * workers - 1) / total);
+  const int pieces = w_last - w0 + 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  float top[8], sum[8], acc[8][kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < pieces; i += kWarps) {
-    const int slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1);
-    const int64_t row = (int64_t)slot * HEADS + h;
-    const float lse = p.part_lse[row];
-    float o[kPer];
+  for (int h = 0; h < 8; ++h) {
+    top[h] = -INFINITY;
+    sum[h] = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) o[k] = p.part_o[row * D + lane * kPer + k];
-    const float now = fmaxf(top, lse), ref = now == -INFINITY ? 0.f : now;
-    const float f = exp2f(top - ref), g = exp2f(lse - ref);
-    top = now;
-    sum = sum * f + g;
+    for (int k = 0; k < kPer; ++k) acc[h][k] = 0.f;
+  }
+  for (int i = warp; i < pieces; i += kJoinWarps) {
+    const int slot = i == 0 ? 2 * (w0 - 1) + 1 : 2 * (w0 + i - 1);
+    const int64_t row = (int64_t)slot * HEADS + h8;
+    float lse[8], o[8][kPer];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = acc[k] * f + g * o[k];
+    for (int h = 0; h < 8; ++h) {
+      lse[h] = h < heads ? p.part_lse[row + h] : -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) o[h][k] = h < heads ? p.part_o[(row + h) * D + lane + 32 * k] : 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      const float now = fmaxf(top[h], lse[h]), ref = now == -INFINITY ? 0.f : now;
+      const float f = ptx::ex2(top[h] - ref), g = ptx::ex2(lse[h] - ref);
+      top[h] = now;
+      sum[h] = sum[h] * f + g;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[h][k] = acc[h][k] * f + g * o[h][k];
+    }
   }
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) part_o[warp][lane * kPer + k] = acc[k];
-  if (lane == 0) {
-    part_max[warp] = top;
-    part_sum[warp] = sum;
+  for (int h = 0; h < 8; ++h) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) part_o[warp][h][lane + 32 * k] = acc[h][k];
+    if (lane == 0) {
+      part_max[warp][h] = top[h];
+      part_sum[warp][h] = sum[h];
+    }
   }
   __syncthreads();
-  float all = part_max[0];
+  static_assert(kJoinWarps == 8, "warp h finishes head h");
+  const int h = warp;
+  if (h >= heads) return;
+  float all = part_max[0][h];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) all = fmaxf(all, part_max[w]);
+  for (int w = 1; w < kJoinWarps; ++w) all = fmaxf(all, part_max[w][h]);
   const bool dead = all == -INFINITY;
-  float l = 0.f;
+  float l = 0.f, o[kPer];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) l += dead ? 0.f : exp2f(part_max[w] - all) * part_sum[w];
-  T* dst = static_cast<T*>(p.o) + (int64_t)rec.b * p.o_tok + (int64_t)(head0 + h) * p.o_head;
-  for (int e = threadIdx.x; e < p.d; e += kThreads) {
-    float o = 0.f;
-    if (!dead) {
+  for (int k = 0; k < kPer; ++k) o[k] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) o += exp2f(part_max[w] - all) * part_o[w][e];
-      o /= l;
-    }
-    dst[e] = from_f<T>(o);
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float f = dead ? 0.f : ptx::ex2(part_max[w][h] - all);
+    l += f * part_sum[w][h];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] += f * part_o[w][h][lane + 32 * k];
   }
-  if (threadIdx.x == 0 && p.stats)
-    p.stats[(int64_t)rec.b * p.stats_tok + (int64_t)(head0 + h) * p.stats_head] =
+  const float inv = dead ? 0.f : 1.f / l;
+  T* dst = static_cast<T*>(p.o) + (int64_t)rec.b * p.o_tok + (int64_t)(head0 + h8 + h) * p.o_head;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (lane + 32 * k < p.d) dst[lane + 32 * k] = from_f<T>(o[k] * inv);
+  if (lane == 0 && p.stats)
+    p.stats[(int64_t)rec.b * p.stats_tok + (int64_t)(head0 + h8 + h) * p.stats_head] =
         dead ? -INFINITY : (all + log2f(l)) * kLn2;
 }
 
@@ -748,7 +793,7 @@ cudaError_t launch_mma(const DecodeParams& p, int ctas, cudaStream_t stream) {
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   paged_decode_mma_kernel<T, D, NT><<<ctas, kThreads, bytes, stream>>>(p);
-  paged_decode_join_kernel<T, D, 8 * NT><<<dim3(ctas, 8 * NT), kThreads, 0, stream>>>(p);
+  paged_decode_join_kernel<T, D, 8 * NT><<<dim3(ctas * kWarps, NT), 32 * kJoinWarps, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -769,10 +814,10 @@ cudaError_t launch_type(const DecodeParams& p, bool mma, int ctas, cudaStream_t 
   }
   if (decode_pad_d(p.d) == 64) {
     paged_decode_simt_kernel<T, 64><<<ctas, kThreads, 0, stream>>>(p);
-    paged_decode_join_kernel<T, 64, 8><<<dim3(ctas, 8), kThreads, 0, stream>>>(p);
+    paged_decode_join_kernel<T, 64, 8><<<ctas * kWarps, 32 * kJoinWarps, 0, stream>>>(p);
   } else {
     paged_decode_simt_kernel<T, 128><<<ctas, kThreads, 0, stream>>>(p);
-    paged_decode_join_kernel<T, 128, 8><<<dim3(ctas, 8), kThreads, 0, stream>>>(p);
+    paged_decode_join_kernel<T, 128, 8><<<ctas * kWarps, 32 * kJoinWarps, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }

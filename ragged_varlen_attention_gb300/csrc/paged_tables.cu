@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(PagedTablesParam
         p.positions[row0 + i] = position[i];
       }
   }
-  write_status(p.status, kPagedTablesMaxBlocks, status);
+  write_status(p.status, status);
 }
 
 }  // namespace
