@@ -269,6 +269,22 @@ __device__ __forceinline__ void write_status(uint32_t* status, uint32_t bits) {
   if (blockIdx.x == 0) status[0] = gridDim.x;
 }
 
+// n / d and n % d for 0 <= n < 2^31 and 1 <= d < 2^31 without a division: with 2^s the
+// least power of two >= d and m = ceil(2^(31+s) / d) < 2^32 + 1, n m / 2^(31+s) exceeds
+// n / d by less than n / 2^(31+s) < 2^-s <= 1/d, so the floors agree.
+struct FastDiv {
+  uint64_t mul;
+  int32_t d, shift;
+  __host__ __device__ FastDiv() {}
+  __host__ explicit FastDiv(int32_t div) : d(div) {
+    int s = 0;
+    while ((int64_t(1) << s) < div) ++s;
+    shift = 31 + s;
+    mul = ((uint64_t(1) << shift) + (uint64_t)div - 1) / (uint64_t)div;
+  }
+  __device__ __forceinline__ int32_t div(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+
 struct NormRopeParams {
   const void* in[4];        // Q, K, then V (paged) or dQ out, dK out (backward)
   void* out[3];             // Q out, K out / K cache, V cache; backward: dQ, dK
@@ -331,6 +347,7 @@ struct DecodeParams {
   int64_t table_stride, stats_tok, stats_head;
   int32_t batch, h_q, h_kv, d, group;
   int32_t page_size, num_pages, max_pages;
+  FastDiv by_page;
   float scale_log2;
   uint32_t* status;
   DecodeRec* recs;          // [workers]

@@ -319,6 +319,7 @@ thd_status_t thd_paged_decode(thd_attn_plan_t plan, const void* q, const void* k
   dp.stats_tok = plan->stats_tok; dp.stats_head = plan->stats_head;
   dp.batch = d.batch; dp.h_q = d.h_q; dp.h_kv = d.h_kv; dp.d = d.d; dp.group = d.h_q / d.h_kv;
   dp.page_size = d.page_size; dp.num_pages = d.num_pages; dp.max_pages = d.max_pages;
+  dp.by_page = thd::FastDiv(d.page_size);
   dp.scale_log2 = plan->scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
   dp.status = reinterpret_cast<uint32_t*>(ws);

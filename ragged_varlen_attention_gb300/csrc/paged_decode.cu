@@ -260,11 +260,13 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 // rounded to the storage type for the product (at most half a step of a value <= 1),
 // its sum is kept in float32.
 //
-// Each lane copies whole rows of one key by bulk copies (K and V of key `lane`; with 16
-// keys a chunk, K by the lower lanes and V by the upper ones), so a page number is used by
-// the lane that looked it up and any page size or stride costs the same. Rows sit 16 bytes
-// apart from a multiple of 128, so that ldmatrix's eight rows fall into different banks
-// without a swizzle, and every address in the loop is a constant away from the stage's.
+// A stage is filled by cp.async, 16 bytes a lane, 2 (d = 128) or 4 rows at a time. Where a
+// page holds a multiple of 16 rows and the whole chunk is visible, its rows are a constant
+// stride apart and cost an addition each; otherwise each row's page comes from the lane that
+// looked it up. Rows sit 16 bytes apart from a multiple of 128, so that ldmatrix's eight rows
+// fall into different banks without a swizzle, and every address in the loop is a constant
+// away from the stage's. (One bulk copy per row instead, by the lane that knows the page, was
+// slower: the copy unit takes 11 to 15 cycles a row, 3.4 TB/s at d = 64, 4.95 at d = 128.)
 template <int D>
 struct MmaSmem {
   static constexpr int kKeys = chunk_keys(D);
@@ -272,18 +274,21 @@ struct MmaSmem {
   static constexpr int kPitch = 2 * D + 16;
   static constexpr int kStageBytes = 2 * kKeys * kPitch;  // K rows, then V rows
   unsigned char ring[kWarps][kStages][kStageBytes];
-  uint64_t full[kWarps][kStages];
   uint32_t seen[kWarps][kStages];  // bit r: key r of the stage is visible
 };
 
-// Waits for a phase of a barrier for at most about 2 s (a copy takes microseconds); false
-// when it gave up.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer_ns();
-  while (!ptx::mbar_try_wait(bar, parity))
-    if (ptx::globaltimer_ns() - t0 > 2000000000ull) return false;
-  return true;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes of zeros when not `real` (src is not read then)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  const int bytes = real ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <typename T, int D, int NT>
@@ -301,18 +306,9 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   const int per = (p.group + kHeads - 1) / kHeads;   // segments of a kv head
   const int segs = p.h_kv * per;
   uint32_t status = 0;
-  const uint32_t ring = ptx::smem_u32(sm.ring[warp]), full = ptx::smem_u32(sm.full[warp]);
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) ptx::mbar_init(full + 8 * i, 1);
-    ptx::fence_mbar_init();
-  }
-  if (p.d < D) {  // the columns that no row copy fills are zeros throughout
-    for (int i = lane; i < (int)sizeof(sm.ring[0]) / 16; i += 32)
-      reinterpret_cast<uint4*>(sm.ring[warp])[i] = make_uint4(0u, 0u, 0u, 0u);
-    ptx::fence_proxy_async_smem();
-  }
+  const uint32_t ring = ptx::smem_u32(sm.ring[warp]);
   Cursor<kKeys> cur;
-  int steps = locate<kKeys>(p, segs, cur, status);
+  const int steps = locate<kKeys>(p, segs, cur, status);
   write_empty<T>(p);
 
   Cursor<kKeys> load = cur;
@@ -326,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
     if (issued >= steps) return;
     const int key = load.sp.base + load.chunk * kKeys + (lane & (kKeys - 1));
     if (key >= load.sp.lo && key < load.sp.n) {
-      const int column = (int)((uint32_t)key / (uint32_t)p.page_size);
+      const int column = p.by_page.div(key);
       key_row = key - column * p.page_size;
       key_page = p.block_table[(int64_t)load.b * p.table_stride + column];
       if (key_page < 0 || key_page >= p.num_pages) {
@@ -335,34 +331,60 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
       }
     }
   };
-  const uint32_t row_bytes = 2 * p.d;
+  constexpr uint32_t kAll = kKeys == 16 ? 0xffffu : 0xffffffffu;
+  constexpr int kVecs = D / 8;             // 16-byte pieces of a row
+  constexpr int kRowsAtOnce = 32 / kVecs;  // rows of one warp-wide copy
+  const int vec = lane % kVecs, row_in = lane / kVecs;
+  const bool vec_real = vec * 8 < p.d;
+  const bool whole_pages = (p.page_size & 15) == 0 && p.d == D;
   auto issue = [&]() {
-    if (issued >= steps) return;
-    const uint32_t seen = __ballot_sync(0xffffffffu, key_page >= 0) & (kKeys == 16 ? 0xffffu : 0xffffffffu);
-    const uint32_t bar = full + 8 * load_stage;
-    if (lane == 0) {
-      sm.seen[warp][load_stage] = seen;
-      ptx::mbar_arrive_expect_tx(bar, 2 * __popc(seen) * row_bytes);
-    }
-    __syncwarp();
-    if (key_page >= 0) {
+    if (issued < steps) {
+      const uint32_t seen = __ballot_sync(0xffffffffu, key_page >= 0) & kAll;
+      if (lane == 0) sm.seen[warp][load_stage] = seen;
+      const uint32_t dst = ring + load_stage * Smem::kStageBytes + row_in * kPitch + vec * 16;
       const int g = load.seg / per;
-      const uint32_t dst = ring + load_stage * Smem::kStageBytes + lane * kPitch;
-      const T* ks = static_cast<const T*>(p.k) + (int64_t)key_page * p.k_page + (int64_t)key_row * p.k_tok + (int64_t)g * p.k_head;
-      const T* vs = static_cast<const T*>(p.v) + (int64_t)key_page * p.v_page + (int64_t)key_row * p.v_tok + (int64_t)g * p.v_head;
-      if (kKeys == 16) {
-        ptx::bulk_load(dst, lane < 16 ? ks : vs, row_bytes, bar);
+      const T* kh = static_cast<const T*>(p.k) + (int64_t)g * p.k_head + vec * 8;
+      const T* vh = static_cast<const T*>(p.v) + (int64_t)g * p.v_head + vec * 8;
+      if (whole_pages && seen == kAll) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int page = __shfl_sync(0xffffffffu, key_page, mt * 16);
+          const int in_page = __shfl_sync(0xffffffffu, key_row, mt * 16) + row_in;
+          const T* ks = kh + (int64_t)page * p.k_page + (int64_t)in_page * p.k_tok;
+          const T* vs = vh + (int64_t)page * p.v_page + (int64_t)in_page * p.v_tok;
+#pragma unroll
+          for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
+            const uint32_t at = dst + (mt * 16 + i * kRowsAtOnce) * kPitch;
+            cp_async16(at, ks);
+            cp_async16(at + kKeys * kPitch, vs);
+            ks += kRowsAtOnce * p.k_tok;
+            vs += kRowsAtOnce * p.v_tok;
+          }
+        }
       } else {
-        ptx::bulk_load(dst, ks, row_bytes, bar);
-        ptx::bulk_load(dst + kKeys * kPitch, vs, row_bytes, bar);
+#pragma unroll
+        for (int i = 0; i < kKeys / kRowsAtOnce; ++i) {
+          const int page = __shfl_sync(0xffffffffu, key_page, i * kRowsAtOnce + row_in);
+          const int in_page = __shfl_sync(0xffffffffu, key_row, i * kRowsAtOnce + row_in);
+          const bool real = page >= 0 && vec_real;
+          const uint32_t at = dst + i * kRowsAtOnce * kPitch;
+          const T* ks = static_cast<const T*>(p.k);
+          const T* vs = static_cast<const T*>(p.v);
+          if (real) {
+            ks = kh + (int64_t)page * p.k_page + (int64_t)in_page * p.k_tok;
+            vs = vh + (int64_t)page * p.v_page + (int64_t)in_page * p.v_tok;
+          }
+          cp_async16(at, ks, real);
+          cp_async16(at + kKeys * kPitch, vs, real);
+        }
       }
+      ++issued;
+      load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
+      load.advance(p, segs, issued < steps);
+      look_up();
     }
-    ++issued;
-    load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
-    load.advance(p, segs, issued < steps);
-    look_up();
+    cp_commit();  // an empty group when there is nothing left: the count stays one per step
   };
-  __syncwarp();
   look_up();
   for (int i = 0; i < kStages - 1; ++i) issue();
 
@@ -371,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   float top[NT][2], sum[NT][2];
   int head0 = 0, heads = 0, first = 0;
   bool fresh = true;
-  uint32_t stage = 0, parity = 0;
+  uint32_t stage = 0;
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
@@ -397,21 +419,11 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
           for (int j = 0; j < 4; ++j) acc[dt][nt][j] = 0.f;
       }
     }
-    if (!wait_phase(full + 8 * stage, parity)) {
-      status |= THD_DEV_WAIT_TIMEOUT;
-      steps = issued;  // no further copies; those in flight are waited for (with the same limit)
-    }
+    cp_wait<kStages - 2>();
+    __syncwarp();
     const uint32_t seen = sm.seen[warp][stage];
     const uint32_t kbase = ring + stage * Smem::kStageBytes;
     const uint32_t vbase = kbase + kKeys * kPitch;
-    if (seen != (kKeys == 16 ? 0xffffu : 0xffffffffu)) {
-      // V rows that were not copied hold anything: 0 x NaN must not reach the sums
-      for (int r = 0; r < kKeys; ++r)
-        if (!((seen >> r) & 1) && lane < D / 8)
-          *reinterpret_cast<uint4*>(sm.ring[warp][stage] + (kKeys + r) * kPitch + lane * 16) = make_uint4(0u, 0u, 0u, 0u);
-      ptx::fence_proxy_async_smem();  // before the next copy into these rows
-      __syncwarp();
-    }
     if (seen != 0) {
       float s[MT][NT][4];
 #pragma unroll
@@ -500,10 +512,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
     }
     __syncwarp();  // the stage is read by every lane before it is filled again
     issue();
-    if (++stage == kStages) {
-      stage = 0;
-      parity ^= 1;
-    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
 
     if (cur.chunk + 1 == cur.sp.chunks || step + 1 == steps) {
       const int slot = piece_slot(worker, first, cur.chunk, cur.sp.chunks);
@@ -599,7 +608,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParam
     {
       const int key = cur.sp.base + cur.chunk * kChunk + (lane & (kChunk - 1));
       if (key >= cur.sp.lo && key < cur.sp.n) {
-        const int column = (int)((uint32_t)key / (uint32_t)p.page_size);
+        const int column = p.by_page.div(key);
         in_page = key - column * p.page_size;
         page = p.block_table[(int64_t)cur.b * p.table_stride + column];
         if (page < 0 || page >= p.num_pages) {
