@@ -249,6 +249,25 @@ constexpr int kBwdKeysPerUnit = 128;   // keys of a dK/dV unit
 cudaError_t launch_bwd_prep(const BwdParams& p, thd_dtype_t dtype, int num_sms, cudaStream_t stream);
 cudaError_t launch_bwd_simt(const BwdParams& p, thd_dtype_t dtype, int num_sms, cudaStream_t stream);
 
+// Launch that may begin while the kernel before it in the stream ends: the launch itself
+// and the blocks' start overlap with that kernel's tail. Every thread of such a kernel
+// executes ptx::pdl_wait() before it touches global memory.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                                     cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // SM count of the current device (0: no device).
 int current_device_sms();
 
@@ -328,10 +347,11 @@ constexpr int kPagedTablesMaxBlocks = kMaxStatusBlocks;
 constexpr int kPagedTablesRowsPerBlock = 1024;
 cudaError_t launch_paged_tables(const PagedTablesParams& p, cudaStream_t stream);
 
-// What the join kernel needs to know of worker (warp) w of a decode launch: the segment
-// its range starts in, that segment's chunks, and how many of them lie before the range.
+// What worker (warp) w of a decode launch leaves for the join kernel: if its range is the
+// first that begins inside a segment, the segment and the number of its pieces, else 0
+// pieces.
 struct DecodeRec {
-  int32_t b, seg, chunks, before;
+  int32_t b, seg, pieces, unused;
 };
 struct DecodeParams {
   const void* q;
@@ -351,7 +371,6 @@ struct DecodeParams {
   float scale_log2;
   uint32_t* status;
   DecodeRec* recs;          // [workers]
-  int64_t* total;           // chunks of the launch, workers that share them
   float* part_o;            // [2 workers][heads of a segment][d padded] normalised partial O
   float* part_lse;          // [2 workers][heads of a segment] base-2 log-sum-exp
 };

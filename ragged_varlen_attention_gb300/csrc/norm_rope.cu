@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace thd {
 
@@ -124,6 +125,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeParams p) {
   const int cq = (p.h_q + kHeads - 1) / kHeads, ck = (p.h_kv + kHeads - 1) / kHeads;
   const int per_token = cq + ck + (kPaged ? ck : 0);
   const int64_t units = (int64_t)p.rows * per_token;
+  ptx::pdl_wait();
+  ptx::pdl_release();
   uint32_t status = 0;
   float dw[2][8];
   if constexpr (kBack) {
@@ -282,6 +285,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeParams 
   const int per_token = p.h_q + p.h_kv * (kPaged ? 2 : 1);
   const int64_t units = (int64_t)p.rows * per_token;
   const int half = p.rot / 2;
+  ptx::pdl_wait();
+  ptx::pdl_release();
   uint32_t status = 0;
   float dw[2][8];
 #pragma unroll
@@ -394,6 +399,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeParams 
 // dw = sum over the blocks' partial rows, 32 columns to a block, in a fixed order.
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(NormRopeParams p, int blocks) {
   __shared__ float part[32][33];
+  ptx::pdl_wait();
+  ptx::pdl_release();
   const int col = blockIdx.x * 32 + threadIdx.x % 32, row = threadIdx.x / 32;
   float v = 0.f;
   if (col < 2 * p.d)
@@ -418,16 +425,13 @@ cudaError_t launch_form(const NormRopeParams& p, bool vec, int num_sms, cudaStre
   const int64_t need = (p.rows * per_token + kWarps - 1) / kWarps;
   int blocks = sms * 8;
   if (need < blocks) blocks = need > 0 ? (int)need : 1;
-  if (!vec) norm_rope_any_kernel<T, FORM><<<blocks, kThreads, 0, stream>>>(p);
-  else if (g == 8) norm_rope_kernel<T, 8, FORM><<<blocks, kThreads, 0, stream>>>(p);
-  else if (g == 16) norm_rope_kernel<T, 16, FORM><<<blocks, kThreads, 0, stream>>>(p);
-  else norm_rope_kernel<T, 32, FORM><<<blocks, kThreads, 0, stream>>>(p);
-  if (FORM == THD_NORM_ROPE_BWD && (p.dw[0] || p.dw[1])) {
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    norm_rope_dw_kernel<<<(2 * p.d + 31) / 32, 1024, 0, stream>>>(p, blocks);
-  }
-  return cudaGetLastError();
+  const auto kernel = !vec ? norm_rope_any_kernel<T, FORM>
+                      : g == 8 ? norm_rope_kernel<T, 8, FORM>
+                      : g == 16 ? norm_rope_kernel<T, 16, FORM>
+                                : norm_rope_kernel<T, 32, FORM>;
+  const cudaError_t e = launch_overlapped(kernel, blocks, kThreads, 0, stream, p);
+  if (e != cudaSuccess || FORM != THD_NORM_ROPE_BWD || !(p.dw[0] || p.dw[1])) return e;
+  return launch_overlapped(norm_rope_dw_kernel, (2 * p.d + 31) / 32, 1024, 0, stream, p, blocks);
 }
 
 template <typename T>

@@ -288,7 +288,6 @@ thd_status_t thd_paged_decode_plan(thd_attn_plan_t* out, const thd_paged_decode_
   const int64_t rows = 2 * (int64_t)thd::kDecodeMaxWorkers * seg_heads;
   int64_t off = align_up(4 * (1 + thd::kDecodeMaxCtas));
   p->ws_off[1] = off; off = align_up(off + thd::kDecodeMaxWorkers * (int64_t)sizeof(thd::DecodeRec));
-  p->ws_off[2] = off; off = align_up(off + 2 * 8);
   p->ws_off[3] = off; off = align_up(off + rows * thd::decode_pad_d(d.d) * 4);
   p->ws_off[4] = off; off = align_up(off + rows * 4);
   p->ws_bytes = (size_t)off;
@@ -324,7 +323,6 @@ thd_status_t thd_paged_decode(thd_attn_plan_t plan, const void* q, const void* k
   char* ws = static_cast<char*>(workspace);
   dp.status = reinterpret_cast<uint32_t*>(ws);
   dp.recs = reinterpret_cast<thd::DecodeRec*>(ws + plan->ws_off[1]);
-  dp.total = reinterpret_cast<int64_t*>(ws + plan->ws_off[2]);
   dp.part_o = reinterpret_cast<float*>(ws + plan->ws_off[3]);
   dp.part_lse = reinterpret_cast<float*>(ws + plan->ws_off[4]);
   const int sms = thd::current_device_sms();

@@ -7,9 +7,9 @@
 // memory bounds the kernel. What matters is that every SM streams at its share of
 // the bandwidth until the end, whatever the lengths are:
 //   - A segment is (request, kv head, up to 8/16/32 query heads of its group). All
-//     segments' key chunks (16 or 32 keys) form one line, and warp w of n takes the
-//     chunks [w W / n, (w + 1) W / n) of it, across segment borders. The border
-//     positions follow from the lengths on the device; no setup kernel, no work list.
+//     segments' key chunks (16 or 32 keys) form one line, which the warps share in equal
+//     ranges, in order and across segment borders. The border positions follow from the
+//     lengths on the device; no setup kernel, no work list.
 //   - A warp streams its chunks through its own ring of stages and keeps its own
 //     running maximum, sum and output: no warp waits for another one.
 //   - A segment that lies inside one warp's range is finished there. One that crosses a
@@ -101,13 +101,23 @@ struct Cursor {
   }
 };
 
-// First chunk of worker (warp) w of n over a line of `total` chunks.
-__device__ __forceinline__ int64_t line_start(int64_t w, int64_t total, int32_t n) { return w * total / n; }
+// The line's `total` chunks over the workers (warps): `each` of them, the first `extra`
+// workers one more.
+struct Line {
+  int64_t total;
+  int32_t workers, each, extra;
+  __device__ __forceinline__ int64_t start(int32_t w) const { return (int64_t)w * each + min(w, extra); }
+  // the worker that holds chunk t
+  __device__ __forceinline__ int32_t holder(int64_t t) const {
+    const int64_t big = (int64_t)extra * (each + 1);
+    return t < big ? (int32_t)(t / (each + 1)) : extra + (int32_t)((t - big) / each);
+  }
+};
 
 // The number of chunks in the warp's range, and the cursor at its beginning. Every thread
-// calls it. Leaves the join kernel's record of each worker.
+// calls it.
 template <int KC>
-__device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC>& cur, uint32_t& status) {
+__device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC>& cur, Line& line, uint32_t& status) {
   __shared__ int64_t warp_sums[kWarps];
   __shared__ int32_t found_b[kWarps];
   __shared__ int64_t found_before[kWarps];
@@ -133,11 +143,14 @@ __device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC
     if (w < warp) upto += warp_sums[w];
     total += warp_sums[w];
   }
-  total *= segs;
-  const int32_t workers = (int32_t)min64((int64_t)gridDim.x * kWarps, max64(total, 1));
+  line.total = total * segs;
+  line.workers = (int32_t)min64((int64_t)gridDim.x * kWarps, max64(line.total, 1));
+  line.each = (int32_t)(line.total / line.workers);  // below 2^31 by the plan's bound
+  line.extra = (int32_t)(line.total - (int64_t)line.each * line.workers);
   // the request that each of the block's workers begins in
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const int64_t at = line_start((int64_t)blockIdx.x * kWarps + w, total, workers);
+    const int64_t at = line.start(blockIdx.x * kWarps + w);
     int64_t before = (upto - mine) * segs;
     if (before <= at && at < upto * segs) {
       for (int b = b0; b < b1; ++b) {
@@ -153,24 +166,27 @@ __device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC
   }
   __syncthreads();
   const int32_t worker = blockIdx.x * kWarps + warp;
+  if (worker >= line.workers || line.total == 0) return 0;
+  cur.b = found_b[warp];
+  cur.sp = span_of<KC>(p, cur.b);
+  const int64_t rel = line.start(worker) - found_before[warp];  // below segs x chunks
+  cur.seg = (int)(rel / cur.sp.chunks);
+  cur.chunk = (int)(rel - (int64_t)cur.seg * cur.sp.chunks);
+  return (int)(line.start(worker + 1) - line.start(worker));
+}
+
+// The worker's record for the join kernel, from the cursor at the beginning of its range.
+template <int KC>
+__device__ __forceinline__ void write_record(const DecodeParams& p, const Line& line, const Cursor<KC>& cur, int steps) {
+  if ((threadIdx.x & 31) != 0) return;
+  const int32_t worker = blockIdx.x * kWarps + threadIdx.x / 32;
   DecodeRec rec = {0, 0, 0, 0};
-  int steps = 0;
-  if (worker < workers && total > 0) {
-    const int64_t begin = line_start(worker, total, workers);
-    steps = (int)(line_start(worker + 1, total, workers) - begin);  // below 2^31 by the plan's bound
-    cur.b = found_b[warp];
-    cur.sp = span_of<KC>(p, cur.b);
-    const int64_t rel = begin - found_before[warp];
-    cur.seg = (int)(rel / cur.sp.chunks);
-    cur.chunk = (int)(rel - (int64_t)cur.seg * cur.sp.chunks);
-    rec = {cur.b, cur.seg, cur.sp.chunks, cur.chunk};
+  if (steps > 0 && cur.chunk > 0) {
+    const int64_t begin = line.start(worker) - cur.chunk;
+    if (line.start(worker - 1) <= begin)
+      rec = {cur.b, cur.seg, line.holder(begin + cur.sp.chunks - 1) - worker + 2, 0};
   }
-  if (lane == 0) p.recs[worker] = rec;
-  if (worker == 0 && lane == 0) {
-    p.total[0] = total;
-    p.total[1] = workers;
-  }
-  return steps;
+  p.recs[worker] = rec;
 }
 
 // Rows without a visible key: O = 0, LSE = -inf.
@@ -305,11 +321,13 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   const int worker = blockIdx.x * kWarps + warp;
   const int per = (p.group + kHeads - 1) / kHeads;   // segments of a kv head
   const int segs = p.h_kv * per;
+  ptx::pdl_wait();
+  ptx::pdl_release();
   uint32_t status = 0;
   const uint32_t ring = ptx::smem_u32(sm.ring[warp]);
   Cursor<kKeys> cur;
-  const int steps = locate<kKeys>(p, segs, cur, status);
-  write_empty<T>(p);
+  Line line;
+  const int steps = locate<kKeys>(p, segs, cur, line, status);
 
   Cursor<kKeys> load = cur;
   int issued = 0;
@@ -387,6 +405,8 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   };
   look_up();
   for (int i = 0; i < kStages - 1; ++i) issue();
+  write_record<kKeys>(p, line, cur, steps);
+  write_empty<T>(p);
 
   uint32_t qf[D / 16][NT][2];
   float acc[D / 16][NT][4];
@@ -576,9 +596,13 @@ __global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParam
   const int worker = blockIdx.x * kWarps + threadIdx.x / 32;
   const int per = (p.group + kHeads - 1) / kHeads;
   const int segs = p.h_kv * per;
+  ptx::pdl_wait();
+  ptx::pdl_release();
   uint32_t status = 0;
   Cursor<kChunk> cur;
-  const int steps = locate<kChunk>(p, segs, cur, status);
+  Line line;
+  const int steps = locate<kChunk>(p, segs, cur, line, status);
+  write_record<kChunk>(p, line, cur, steps);
   write_empty<T>(p);
 
   float q[8][kPer], acc[8][kPer], top[8], sum[8];
@@ -714,21 +738,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_decode_join_kernel(Deco
   constexpr int kPer = D / 32;
   __shared__ float part_o[kJoinWarps][8][D];
   __shared__ float part_max[kJoinWarps][8], part_sum[kJoinWarps][8];
-  const int64_t total = p.total[0];
-  const int32_t workers = (int32_t)p.total[1];
+  ptx::pdl_wait();
+  ptx::pdl_release();
   const int w0 = blockIdx.x;
-  if (w0 == 0 || w0 >= workers || total == 0) return;
   const DecodeRec rec = p.recs[w0];
-  if (rec.before == 0) return;
-  const int64_t begin = line_start(w0, total, workers) - rec.before, end = begin + rec.chunks;
-  if (line_start(w0 - 1, total, workers) > begin) return;  // an earlier block's
+  const int pieces = rec.pieces;
+  if (pieces == 0) return;
   int head0;
   const int h8 = blockIdx.y * 8;
   const int heads = segment_heads<HEADS>(p, rec.seg, head0) - h8;
   if (heads <= 0) return;
-  // the worker that holds the segment's last chunk
-  const int w_last = (int)((end * workers - 1) / total);
-  const int pieces = w_last - w0 + 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   float top[8], sum[8], acc[8][kPer];
 #pragma unroll
@@ -798,12 +817,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_decode_join_kernel(Deco
 template <typename T, int D, int NT>
 cudaError_t launch_mma(const DecodeParams& p, int ctas, cudaStream_t stream) {
   constexpr int bytes = (int)sizeof(MmaSmem<D>);
-  const cudaError_t e = cudaFuncSetAttribute(paged_decode_mma_kernel<T, D, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_mma_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       bytes);
   if (e != cudaSuccess) return e;
-  paged_decode_mma_kernel<T, D, NT><<<ctas, kThreads, bytes, stream>>>(p);
-  paged_decode_join_kernel<T, D, 8 * NT><<<dim3(ctas * kWarps, NT), 32 * kJoinWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  e = launch_overlapped(paged_decode_mma_kernel<T, D, NT>, ctas, kThreads, bytes, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(paged_decode_join_kernel<T, D, 8 * NT>, dim3(ctas * kWarps, NT), 32 * kJoinWarps, 0, stream, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_simt(const DecodeParams& p, int ctas, cudaStream_t stream) {
+  const cudaError_t e = launch_overlapped(paged_decode_simt_kernel<T, D>, ctas, kThreads, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(paged_decode_join_kernel<T, D, 8>, ctas * kWarps, 32 * kJoinWarps, 0, stream, p);
 }
 
 template <typename T, int D>
@@ -821,14 +847,7 @@ cudaError_t launch_type(const DecodeParams& p, bool mma, int ctas, cudaStream_t 
     if (mma) return decode_pad_d(p.d) == 64 ? launch_mma_heads<T, 64>(p, ctas, stream)
                                             : launch_mma_heads<T, 128>(p, ctas, stream);
   }
-  if (decode_pad_d(p.d) == 64) {
-    paged_decode_simt_kernel<T, 64><<<ctas, kThreads, 0, stream>>>(p);
-    paged_decode_join_kernel<T, 64, 8><<<ctas * kWarps, 32 * kJoinWarps, 0, stream>>>(p);
-  } else {
-    paged_decode_simt_kernel<T, 128><<<ctas, kThreads, 0, stream>>>(p);
-    paged_decode_join_kernel<T, 128, 8><<<ctas * kWarps, 32 * kJoinWarps, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  return decode_pad_d(p.d) == 64 ? launch_simt<T, 64>(p, ctas, stream) : launch_simt<T, 128>(p, ctas, stream);
 }
 
 }  // namespace

@@ -10,6 +10,7 @@
 // written first: an old page from the table, a new one from the free list. The token
 // at the start of a new page writes the page's table entry, so nothing else has to.
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace thd {
 
@@ -54,6 +55,8 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(PagedTablesParam
   // -1 for a request that takes no part
   __shared__ int32_t start[kPagedMaxBatch];
   __shared__ int64_t warp_sums[kThreads / 32];
+  ptx::pdl_wait();
+  ptx::pdl_release();
   uint32_t status = 0;
   const int strip = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.batch, (int)threadIdx.x * strip), b1 = min(p.batch, b0 + strip);
@@ -171,8 +174,7 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(PagedTablesParam
 
 cudaError_t launch_paged_tables(const PagedTablesParams& p, cudaStream_t stream) {
   const int blocks = p.cap_rows > 0 ? (p.cap_rows + kPagedTablesRowsPerBlock - 1) / kPagedTablesRowsPerBlock : 1;
-  paged_tables_kernel<<<blocks, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(paged_tables_kernel, blocks, kThreads, 0, stream, p);
 }
 
 }  // namespace thd
