@@ -317,6 +317,7 @@ struct NormRopeParams {
   int64_t out_page[3], out_tok[3], out_head[3];
   int32_t rows, h_q, h_kv, d, rot, interleaved, max_pos;
   int32_t page_size;
+  FastDiv by_heads[2];      // h_q, h_kv
   int64_t num_slots;        // num_pages * page_size
   float eps;
   int32_t zero_skipped;
@@ -324,9 +325,14 @@ struct NormRopeParams {
 };
 constexpr int kNormRopeMaxBlocks = 8 * kMaxSmsForSizing;
 static_assert(kNormRopeMaxBlocks <= kMaxStatusBlocks, "status words");
-// `vec`: every view, weight and the table allow 4-element accesses and rot % 8 == d % 8 == 0
-cudaError_t launch_norm_rope(const NormRopeParams& p, thd_dtype_t dtype, thd_norm_rope_form_t form, bool vec,
-                             int num_sms, cudaStream_t stream);
+// `vec`: every view, weight and the table allow 4-element accesses, rot % 8 == d % 8 == 0,
+// and the rows x heads of a tensor are numbered in 31 bits
+cudaError_t launch_norm_rope_bf16(const NormRopeParams& p, thd_norm_rope_form_t form, bool vec, int num_sms,
+                                  cudaStream_t stream);
+cudaError_t launch_norm_rope_fp16(const NormRopeParams& p, thd_norm_rope_form_t form, bool vec, int num_sms,
+                                  cudaStream_t stream);
+cudaError_t launch_norm_rope_fp32(const NormRopeParams& p, thd_norm_rope_form_t form, bool vec, int num_sms,
+                                  cudaStream_t stream);
 
 struct PagedTablesParams {
   const int32_t* seq_lens;

@@ -1,0 +1,572 @@
+// Per-head RMS norm with the position rotation: forward, backward, and the serving
+// form that writes K and V into the paged cache.
+//
+//   r = 1/sqrt(mean x^2 + eps), y = x r w, z = R(pos) y on the first rot elements
+//   backward: g = R(pos)^T dz, a = g w, xh = x r, dx = r (a - xh mean(a xh)), dw = sum g xh
+//
+// Every element is read once and written once; the arithmetic is a few fma per
+// element, so memory bounds all three forms. A head's row is one group of G = 8 .. 32
+// lanes with 8 elements each, and its sums are shuffles inside the group. A rotated
+// pair never leaves its lane: in the halves layout lane i holds elements 4i .. 4i+3
+// and their partners rot/2 + 4i .., in the adjacent layout 8i .. 8i+7; either way as
+// four a's and their four b's, in packed pairs (half the fma instructions; with scalar
+// ones the backward was bound by them, 41 % of the copy bandwidth). A warp's unit is kUnroll x
+// (32/G) consecutive rows of one tensor, and the next unit's rows are loaded before
+// this one's are computed, so that loads are always in flight.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace thd {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+// rows in flight for each group of lanes: 4, as far as the registers hold two such sets
+constexpr int norm_rope_unroll(int elem, bool back) { return back && elem == 4 ? 2 : 4; }
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// A lane's 8 elements of a row as loaded: 4 from e0, 4 from e1.
+template <typename T>
+struct Raw {
+  uint2 lo, hi;
+  __device__ __forceinline__ void load(const T* row, int e0, int e1) {
+    lo = *reinterpret_cast<const uint2*>(row + e0);
+    hi = *reinterpret_cast<const uint2*>(row + e1);
+  }
+  __device__ __forceinline__ void zero() { lo = hi = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void store(T* row, int e0, int e1) const {
+    *reinterpret_cast<uint2*>(row + e0) = lo;
+    *reinterpret_cast<uint2*>(row + e1) = hi;
+  }
+};
+template <>
+struct Raw<float> {
+  float4 lo, hi;
+  __device__ __forceinline__ void load(const float* row, int e0, int e1) {
+    lo = *reinterpret_cast<const float4*>(row + e0);
+    hi = *reinterpret_cast<const float4*>(row + e1);
+  }
+  __device__ __forceinline__ void zero() { lo = hi = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void store(float* row, int e0, int e1) const {
+    *reinterpret_cast<float4*>(row + e0) = lo;
+    *reinterpret_cast<float4*>(row + e1) = hi;
+  }
+};
+
+// the two elements of a 32-bit word
+template <typename T>
+__device__ __forceinline__ float2 split(uint32_t w);
+template <>
+__device__ __forceinline__ float2 split<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 split<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t merge(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t merge<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t merge<__half>(float x, float y) {
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The lane's elements as pairs (a_k, b_k), k = 0 .. 3, in packed float32:
+// v[0] = (a_0, a_1), v[1] = (a_2, a_3), v[2] = (b_0, b_1), v[3] = (b_2, b_3).
+// Halves layout: a from lo, b from hi. ADJ: lo = a_0 b_0 a_1 b_1, hi = a_2 b_2 a_3 b_3.
+struct Eight {
+  uint64_t v[4];
+  template <typename T, bool ADJ>
+  __device__ __forceinline__ void get(const Raw<T>& r) {
+    float2 x[4];
+    if constexpr (sizeof(T) == 2) {
+      x[0] = split<T>(r.lo.x); x[1] = split<T>(r.lo.y); x[2] = split<T>(r.hi.x); x[3] = split<T>(r.hi.y);
+    } else {
+      x[0] = make_float2(r.lo.x, r.lo.y); x[1] = make_float2(r.lo.z, r.lo.w);
+      x[2] = make_float2(r.hi.x, r.hi.y); x[3] = make_float2(r.hi.z, r.hi.w);
+    }
+    if (ADJ) {
+      v[0] = ptx::f2_pack(x[0].x, x[1].x); v[1] = ptx::f2_pack(x[2].x, x[3].x);
+      v[2] = ptx::f2_pack(x[0].y, x[1].y); v[3] = ptx::f2_pack(x[2].y, x[3].y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = ptx::f2_pack(x[i].x, x[i].y);
+    }
+  }
+  template <typename T, bool ADJ>
+  __device__ __forceinline__ void put(Raw<T>& r) const {
+    float2 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ptx::f2_unpack(v[i], y[i].x, y[i].y);
+    if (ADJ) {
+      x[0] = make_float2(y[0].x, y[2].x); x[1] = make_float2(y[0].y, y[2].y);
+      x[2] = make_float2(y[1].x, y[3].x); x[3] = make_float2(y[1].y, y[3].y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = y[i];
+    }
+    if constexpr (sizeof(T) == 2) {
+      r.lo = make_uint2(merge<T>(x[0].x, x[0].y), merge<T>(x[1].x, x[1].y));
+      r.hi = make_uint2(merge<T>(x[2].x, x[2].y), merge<T>(x[3].x, x[3].y));
+    } else {
+      r.lo = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+      r.hi = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+    }
+  }
+};
+
+__device__ __forceinline__ uint64_t both(float x) { return ptx::f2_pack(x, x); }
+__device__ __forceinline__ float fold(uint64_t x) {
+  float a, b;
+  ptx::f2_unpack(x, a, b);
+  return a + b;
+}
+// <x, y> over the lane's elements
+__device__ __forceinline__ float dot(const Eight& x, const Eight& y) {
+  return fold(ptx::f2_fma(x.v[3], y.v[3], ptx::f2_fma(x.v[2], y.v[2], ptx::f2_fma(x.v[1], y.v[1], ptx::f2_mul(x.v[0], y.v[0])))));
+}
+
+// The angles of a lane's four pairs; neg = -sin.
+struct Angles {
+  uint64_t cos[2], sin[2], neg[2];
+  __device__ __forceinline__ void load(const float* row, int half) {
+    const float4 c = *reinterpret_cast<const float4*>(row), s = *reinterpret_cast<const float4*>(row + half);
+    cos[0] = ptx::f2_pack(c.x, c.y); cos[1] = ptx::f2_pack(c.z, c.w);
+    sin[0] = ptx::f2_pack(s.x, s.y); sin[1] = ptx::f2_pack(s.z, s.w);
+    neg[0] = ptx::f2_pack(-s.x, -s.y); neg[1] = ptx::f2_pack(-s.z, -s.w);
+  }
+  // (a, b) -> (a c - b s, b c + a s), or by the opposite angle
+  template <bool BACK>
+  __device__ __forceinline__ void turn(Eight& y) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t a = y.v[i], b = y.v[2 + i];
+      y.v[i] = ptx::f2_fma(a, cos[i], ptx::f2_mul(b, BACK ? sin[i] : neg[i]));
+      y.v[2 + i] = ptx::f2_fma(b, cos[i], ptx::f2_mul(a, BACK ? neg[i] : sin[i]));
+    }
+  }
+};
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int s = G / 2; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  return v;
+}
+
+// The cache row that row t of tensor `which` (1 K, 2 V) goes to; false: it goes nowhere.
+template <typename T>
+__device__ __forceinline__ bool cache_row(const NormRopeParams& p, int which, int slot, T*& dst) {
+  if (slot < 0 || slot >= p.num_slots) return false;
+  const int page = slot / p.page_size;
+  dst = static_cast<T*>(p.out[which]) + (int64_t)page * p.out_page[which] +
+        (int64_t)(slot - page * p.page_size) * p.out_tok[which];
+  return true;
+}
+
+// One tensor's rows (WHICH: 0 Q, 1 K, 2 V) among the launch's units. `u` is the warp's first
+// unit counted from the tensor's; on return, counted from the next tensor's. ONE: the heads
+// are a multiple of a unit's rows, so that a unit is of one token, with one position and one
+// row of the table. `acc`: the lane's part of the weight gradient (backward).
+template <typename T, int G, int FORM, bool ADJ, bool ONE, int WHICH>
+__device__ __forceinline__ void rows_of(const NormRopeParams& p, int64_t& u, Eight& acc, uint32_t& status) {
+  constexpr bool kBack = FORM == THD_NORM_ROPE_BWD;
+  constexpr bool kCached = FORM == THD_NORM_ROPE_PAGED && WHICH != 0;  // rows go to the cache
+  constexpr int kUnroll = norm_rope_unroll(sizeof(T), kBack);
+  constexpr int kAtOnce = 32 / G;
+  constexpr int kRows = kAtOnce * kUnroll;
+  const int lane = threadIdx.x & 31;
+  const int item = lane % G, sub = lane / G;
+  const bool active = item * 8 < p.d;
+  const bool rotated = item * 8 < p.rot;
+  const int e0 = rotated && !ADJ ? 4 * item : 8 * item;
+  const int e1 = rotated && !ADJ ? p.rot / 2 + 4 * item : 8 * item + 4;
+  const float inv_d = 1.f / (float)p.d;
+  const FastDiv by_heads = p.by_heads[WHICH ? 1 : 0];
+  const int rows = p.rows * by_heads.d;  // below 2^31 by the caller's choice of kernel
+  const int64_t units = (rows + kRows - 1) / kRows;
+  const int64_t stride = (int64_t)gridDim.x * kWarps;
+
+  Eight w;
+  if constexpr (WHICH < 2) {
+    Raw<T> r;
+    if (p.w[WHICH] && active) {
+      r.load(static_cast<const T*>(p.w[WHICH]), e0, e1);
+      w.get<T, ADJ>(r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.v[i] = both(1.f);
+    }
+  }
+
+  struct Unit {
+    Raw<T> x[kUnroll], g[kBack ? kUnroll : 1];
+    int pos[ONE ? 1 : kUnroll];
+  };
+  const auto load = [&](Unit& n, int64_t unit) {
+    const int row0 = (int)unit * kRows + sub;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int row = row0 + i * kAtOnce;
+      const int t = by_heads.div(ONE ? (int)unit * kRows : min(row, rows - 1)), h = row - t * by_heads.d;
+      if (i == 0 || !ONE) n.pos[ONE ? 0 : i] = p.positions[t];
+      if (active && row < rows) {
+        n.x[i].load(static_cast<const T*>(p.in[WHICH]) + (int64_t)t * p.in_tok[WHICH] + (int64_t)h * p.in_head[WHICH], e0,
+                    e1);
+        if constexpr (kBack)
+          n.g[i].load(static_cast<const T*>(p.in[2 + WHICH]) + (int64_t)t * p.in_tok[2 + WHICH] +
+                          (int64_t)h * p.in_head[2 + WHICH],
+                      e0, e1);
+      } else {
+        n.x[i].zero();
+        if constexpr (kBack) n.g[i].zero();
+      }
+    }
+  };
+  Unit next;
+  if (u < units) load(next, u);
+  for (; u < units; u += stride) {
+    Unit now = next;
+    if (u + stride < units) load(next, u + stride);
+    const int row0 = (int)u * kRows + sub;
+    // where the rows go, and the angles: all rows' loads before the first is used
+    T* dst[kUnroll];
+    bool write[kUnroll], skip[kUnroll];
+    Angles angles[ONE || WHICH == 2 ? 1 : kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int row = row0 + i * kAtOnce;
+      const int t = by_heads.div(ONE ? (int)u * kRows : min(row, rows - 1)), h = row - t * by_heads.d;
+      const int pos = now.pos[ONE ? 0 : i];
+      skip[i] = pos < 0 || pos >= p.max_pos;
+      if (pos >= p.max_pos) status |= THD_DEV_BAD_POSITION;
+      if constexpr (kCached) {
+        const int slot = p.slot_map[t];
+        if (slot >= p.num_slots) status |= THD_DEV_BAD_PAGE;
+        write[i] = !skip[i] && cache_row(p, WHICH, slot, dst[i]);
+      } else {
+        dst[i] = static_cast<T*>(p.out[WHICH]) + (int64_t)t * p.out_tok[WHICH];
+        write[i] = !skip[i] || p.zero_skipped;
+      }
+      write[i] = write[i] && active && row < rows;
+      dst[i] += (int64_t)h * p.out_head[WHICH];
+      if constexpr (WHICH < 2)
+        if ((i == 0 || !ONE) && rotated && !skip[i])
+          angles[ONE ? 0 : i].load(p.cos_sin + (int64_t)pos * p.rot + 4 * item, p.rot / 2);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      if constexpr (WHICH < 2) {
+        Eight x;
+        x.get<T, ADJ>(now.x[i]);
+        const float r = rsqrtf(group_sum<G>(dot(x, x)) * inv_d + p.eps);
+        if constexpr (!kBack) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x.v[k] = ptx::f2_mul(ptx::f2_mul(x.v[k], both(r)), w.v[k]);
+          if (rotated && !skip[i]) angles[ONE ? 0 : i].template turn<false>(x);
+        } else {
+          Eight g, a;
+          g.get<T, ADJ>(now.g[i]);
+          if (rotated && !skip[i]) angles[ONE ? 0 : i].template turn<true>(g);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) a.v[k] = ptx::f2_mul(g.v[k], w.v[k]);
+          const float mean = group_sum<G>(dot(a, x)) * r * inv_d;
+          const bool counts = !skip[i] && row0 + i * kAtOnce < rows;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t xh = ptx::f2_mul(x.v[k], both(r));
+            if (counts) acc.v[k] = ptx::f2_fma(g.v[k], xh, acc.v[k]);
+            x.v[k] = ptx::f2_mul(ptx::f2_fma(xh, both(-mean), a.v[k]), both(r));
+          }
+        }
+        if (skip[i]) {
+          now.x[i].zero();
+        } else {
+          x.put<T, ADJ>(now.x[i]);
+        }
+      }
+      if (write[i]) now.x[i].store(dst[i], e0, e1);
+    }
+  }
+  u -= units;
+}
+
+// Blocks of an SM: with the next unit in flight, 24 warps of 2 KB (16 bits, forward) or 12
+// of 4 to 8 KB keep more than the 45 KB in flight that the memory's latency takes.
+constexpr int norm_rope_blocks(int elem, int form, bool one) {
+  return form == THD_NORM_ROPE_BWD || elem == 4 || !one ? 3 : form == THD_NORM_ROPE_PAGED ? 5 : 6;
+}
+
+template <typename T, int G, int FORM, bool ADJ, bool ONE>
+__global__ void __launch_bounds__(kThreads, norm_rope_blocks(sizeof(T), FORM, ONE))
+    norm_rope_kernel(NormRopeParams p) {
+  constexpr bool kBack = FORM == THD_NORM_ROPE_BWD;
+  ptx::pdl_wait();
+  ptx::pdl_release();
+  __shared__ float part[kBack ? kWarps : 1][2][kBack ? G * 8 : 1];
+  uint32_t status = 0;
+  int64_t u = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  Eight acc;
+  // the block's weight gradients: over the warp's groups, then over the warps in order
+  const auto flush = [&](int which) {
+    const int lane = threadIdx.x & 31, item = lane % G;
+    const bool rotated = item * 8 < p.rot;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float v[2];
+      ptx::f2_unpack(acc.v[k], v[0], v[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int s = G; s < 32; s <<= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], s);
+        // pair number and half of v[j], see Eight
+        const int pair = (k & 1) * 2 + j, b = k >> 1;
+        const int e = ADJ ? 8 * item + 2 * pair + b
+                          : rotated ? (b ? p.rot / 2 : 0) + 4 * item + pair : 8 * item + 4 * b + pair;
+        if (lane < G && item * 8 < p.d) part[threadIdx.x / 32][which][e] = v[j];
+      }
+      acc.v[k] = 0;
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc.v[k] = 0;
+  rows_of<T, G, FORM, ADJ, ONE, 0>(p, u, acc, status);
+  if constexpr (kBack) flush(0);
+  rows_of<T, G, FORM, ADJ, ONE, 1>(p, u, acc, status);
+  if constexpr (kBack) {
+    flush(1);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
+      const int j = i / p.d, e = i - j * p.d;
+      float v = 0.f;
+#pragma unroll
+      for (int wp = 0; wp < kWarps; ++wp) v += part[wp][j][e];
+      p.part_dw[(int64_t)blockIdx.x * 2 * p.d + i] = v;
+    }
+  }
+  if constexpr (FORM == THD_NORM_ROPE_PAGED) rows_of<T, G, FORM, ADJ, ONE, 2>(p, u, acc, status);
+  write_status(p.status, status);
+}
+
+// Any d <= 256, any rot, any strides: a warp per (row, head), elements strided over
+// the lanes, partners exchanged through shared memory.
+template <typename T, int FORM>
+__global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeParams p) {
+  constexpr bool kBack = FORM == THD_NORM_ROPE_BWD;
+  constexpr bool kPaged = FORM == THD_NORM_ROPE_PAGED;
+  __shared__ float buf[kWarps][256];
+  __shared__ float part[kBack ? kWarps : 1][2][kBack ? 256 : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int per_token = p.h_q + p.h_kv * (kPaged ? 2 : 1);
+  const int64_t units = (int64_t)p.rows * per_token;
+  const int half = p.rot / 2;
+  ptx::pdl_wait();
+  ptx::pdl_release();
+  uint32_t status = 0;
+  float dw[2][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
+
+  for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
+    const int t = (int)(u / per_token);
+    int h = (int)(u - (int64_t)t * per_token);
+    const int which = h < p.h_q ? 0 : h < p.h_q + p.h_kv ? 1 : 2;
+    h -= which == 0 ? 0 : which == 1 ? p.h_q : p.h_q + p.h_kv;
+    const int pos = p.positions[t];
+    const bool skip = pos < 0 || pos >= p.max_pos;
+    if (pos >= p.max_pos) status |= THD_DEV_BAD_POSITION;
+    T* dst;
+    bool write;
+    if (kPaged && which != 0) {
+      const int slot = p.slot_map[t];
+      if (slot >= p.num_slots) status |= THD_DEV_BAD_PAGE;
+      write = !skip && cache_row(p, which, slot, dst);
+    } else {
+      dst = static_cast<T*>(p.out[which]) + (int64_t)t * p.out_tok[which];
+      write = !skip || p.zero_skipped;
+    }
+    if (!write) continue;
+    dst += (int64_t)h * p.out_head[which];
+    const T* x = static_cast<const T*>(p.in[which]) + (int64_t)t * p.in_tok[which] + (int64_t)h * p.in_head[which];
+    if (which == 2) {
+      for (int e = lane; e < p.d; e += 32) dst[e] = x[e];
+      continue;
+    }
+    if (skip) {
+      for (int e = lane; e < p.d; e += 32) dst[e] = from_f<T>(0.f);
+      continue;
+    }
+    const T* wr = static_cast<const T*>(p.w[which]);
+    const float* angles = p.cos_sin + (int64_t)pos * p.rot;
+    float v[8], w[8], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      v[i] = e < p.d ? to_f(x[e]) : 0.f;
+      w[i] = e < p.d && wr ? to_f(wr[e]) : 1.f;
+      ss += v[i] * v[i];
+    }
+    const float r = rsqrtf(group_sum<32>(ss) / (float)p.d + p.eps);
+    const T* gz = nullptr;
+    if constexpr (kBack)
+      gz = static_cast<const T*>(p.in[2 + which]) + (int64_t)t * p.in_tok[2 + which] +
+           (int64_t)h * p.in_head[2 + which];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      if (e < p.d) buf[warp][e] = kBack ? to_f(gz[e]) : v[i] * r * w[i];
+    }
+    __syncwarp();
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      if (e >= p.d) {
+        z[i] = 0.f;
+      } else if (e >= p.rot) {
+        z[i] = buf[warp][e];
+      } else {
+        const int pair = p.interleaved ? e / 2 : (e < half ? e : e - half);
+        const bool first = p.interleaved ? (e & 1) == 0 : e < half;
+        const int other = p.interleaved ? (e ^ 1) : (first ? e + half : e - half);
+        const float sn = kBack ? -angles[half + pair] : angles[half + pair];
+        const float mine = buf[warp][e], theirs = buf[warp][other];
+        z[i] = first ? mine * angles[pair] - theirs * sn : mine * angles[pair] + theirs * sn;
+      }
+    }
+    if constexpr (kBack) {
+      float ax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ax += z[i] * w[i] * v[i];
+      const float mean = group_sum<32>(ax) * r / (float)p.d;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = v[i] * r, gx = z[i] * xh;
+        dw[0][i] += which == 0 ? gx : 0.f;
+        dw[1][i] += which == 0 ? 0.f : gx;
+        z[i] = r * (z[i] * w[i] - xh * mean);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      if (e < p.d) dst[e] = from_f<T>(z[i]);
+    }
+  }
+  if constexpr (kBack) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[warp][j][lane + 32 * i] = dw[j][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
+      const int j = i / p.d, e = i - j * p.d;
+      float s = 0.f;
+#pragma unroll
+      for (int wp = 0; wp < kWarps; ++wp) s += part[wp][j][e];
+      p.part_dw[(int64_t)blockIdx.x * 2 * p.d + i] = s;
+    }
+  }
+  write_status(p.status, status);
+}
+
+// dw = sum over the blocks' partial rows, 32 columns to a block, in a fixed order.
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(NormRopeParams p, int blocks) {
+  __shared__ float part[32][33];
+  ptx::pdl_wait();
+  ptx::pdl_release();
+  const int col = blockIdx.x * 32 + threadIdx.x % 32, row = threadIdx.x / 32;
+  float v = 0.f;
+  if (col < 2 * p.d)
+    for (int b = row; b < blocks; b += 32) v += p.part_dw[(int64_t)b * 2 * p.d + col];
+  part[row][threadIdx.x % 32] = v;
+  __syncthreads();
+  v = group_sum<32>(part[threadIdx.x % 32][row]);
+  const int c = blockIdx.x * 32 + row;
+  if (threadIdx.x % 32 == 0 && c < 2 * p.d) {
+    float* dw = p.dw[c < p.d ? 0 : 1];
+    if (dw) dw[c < p.d ? c : c - p.d] = v;
+  }
+}
+
+template <typename T, int G, int FORM, bool ADJ>
+cudaError_t launch_vec(const NormRopeParams& p, int sms, cudaStream_t stream, int& blocks) {
+  constexpr int kRows = 32 / G * norm_rope_unroll(sizeof(T), FORM == THD_NORM_ROPE_BWD);
+  const bool one = G < 32 && p.h_q % kRows == 0 && p.h_kv % kRows == 0;
+  const int64_t tensors = FORM == THD_NORM_ROPE_PAGED ? 2 : 1;
+  const int64_t units = ((int64_t)p.rows * p.h_q + kRows - 1) / kRows +
+                        tensors * (((int64_t)p.rows * p.h_kv + kRows - 1) / kRows);
+  blocks = sms * norm_rope_blocks(sizeof(T), FORM, one);
+  if (units < (int64_t)blocks * kWarps) blocks = units > 0 ? (int)((units + kWarps - 1) / kWarps) : 1;
+  if constexpr (G < 32)
+    if (one) return launch_overlapped(norm_rope_kernel<T, G, FORM, ADJ, true>, blocks, kThreads, 0, stream, p);
+  return launch_overlapped(norm_rope_kernel<T, G, FORM, ADJ, false>, blocks, kThreads, 0, stream, p);
+}
+
+template <typename T, int FORM>
+cudaError_t launch_form(const NormRopeParams& p, bool vec, int num_sms, cudaStream_t stream) {
+  const int sms = num_sms < kMaxSmsForSizing ? num_sms : kMaxSmsForSizing;
+  int blocks = 1;
+  cudaError_t e;
+  if (!vec) {
+    const int64_t units = (int64_t)p.rows * (p.h_q + (int64_t)p.h_kv * (FORM == THD_NORM_ROPE_PAGED ? 2 : 1));
+    blocks = sms * 8;
+    if (units < (int64_t)blocks * kWarps) blocks = units > 0 ? (int)((units + kWarps - 1) / kWarps) : 1;
+    e = launch_overlapped(norm_rope_any_kernel<T, FORM>, blocks, kThreads, 0, stream, p);
+  } else if (p.interleaved) {
+    e = p.d <= 64    ? launch_vec<T, 8, FORM, true>(p, sms, stream, blocks)
+        : p.d <= 128 ? launch_vec<T, 16, FORM, true>(p, sms, stream, blocks)
+                     : launch_vec<T, 32, FORM, true>(p, sms, stream, blocks);
+  } else {
+    e = p.d <= 64    ? launch_vec<T, 8, FORM, false>(p, sms, stream, blocks)
+        : p.d <= 128 ? launch_vec<T, 16, FORM, false>(p, sms, stream, blocks)
+                     : launch_vec<T, 32, FORM, false>(p, sms, stream, blocks);
+  }
+  if (e != cudaSuccess || FORM != THD_NORM_ROPE_BWD || !(p.dw[0] || p.dw[1])) return e;
+  return launch_overlapped(norm_rope_dw_kernel, (2 * p.d + 31) / 32, 1024, 0, stream, p, blocks);
+}
+
+}  // namespace
+
+// The operator for one storage type: included by one source file for each.
+template <typename T>
+cudaError_t norm_rope_type(const NormRopeParams& p, thd_norm_rope_form_t form, bool vec, int num_sms,
+                           cudaStream_t stream) {
+  switch (form) {
+    case THD_NORM_ROPE_FWD: return launch_form<T, THD_NORM_ROPE_FWD>(p, vec, num_sms, stream);
+    case THD_NORM_ROPE_BWD: return launch_form<T, THD_NORM_ROPE_BWD>(p, vec, num_sms, stream);
+    default: return launch_form<T, THD_NORM_ROPE_PAGED>(p, vec, num_sms, stream);
+  }
+}
+
+}  // namespace thd

@@ -114,7 +114,9 @@ thd_status_t run_norm_rope(thd_attn_plan_t plan, const void* const (&views)[6], 
   const int out_view[3] = {back ? 4 : 3, back ? 5 : 4, 5};
   const int inputs = back ? 4 : paged ? 3 : 2, outputs = paged ? 3 : 2;
   const int64_t vec_bytes = 4 * plan->elem_bytes;
-  bool vec = d.d % 8 == 0 && d.rot % 8 == 0 && aligned(cos_sin, 16) && aligned(w_q, vec_bytes) &&
+  const int64_t most_heads = d.h_q > d.h_kv ? d.h_q : d.h_kv;
+  // 64 spare: the last unit's rows are numbered past the tensor's end
+  bool vec = d.d % 8 == 0 && d.rot % 8 == 0 && d.rows * most_heads < kInt32End - 64 && aligned(cos_sin, 16) && aligned(w_q, vec_bytes) &&
              aligned(w_k, vec_bytes);
   for (int i = 0; i < inputs; ++i) {
     const int v = in_view[i];
@@ -139,6 +141,8 @@ thd_status_t run_norm_rope(thd_attn_plan_t plan, const void* const (&views)[6], 
   np.part_dw = reinterpret_cast<float*>(ws + plan->ws_off[1]);
   np.dw[0] = dw_q; np.dw[1] = dw_k;
   np.rows = d.rows; np.h_q = d.h_q; np.h_kv = d.h_kv; np.d = d.d; np.rot = d.rot;
+  np.by_heads[0] = thd::FastDiv(d.h_q);
+  np.by_heads[1] = thd::FastDiv(d.h_kv);
   np.interleaved = d.interleaved ? 1 : 0;
   np.max_pos = d.max_pos;
   np.page_size = d.page_size;
@@ -147,9 +151,10 @@ thd_status_t run_norm_rope(thd_attn_plan_t plan, const void* const (&views)[6], 
   np.zero_skipped = (d.flags & THD_FLAG_ZERO_SKIPPED) ? 1 : 0;
   const int sms = thd::current_device_sms();
   if (sms <= 0) return THD_ERR_CUDA;
-  return thd::launch_norm_rope(np, d.dtype, d.form, vec, sms, static_cast<cudaStream_t>(stream_ptr)) == cudaSuccess
-             ? THD_OK
-             : THD_ERR_CUDA;
+  const auto launch = d.dtype == THD_BF16   ? thd::launch_norm_rope_bf16
+                      : d.dtype == THD_FP16 ? thd::launch_norm_rope_fp16
+                                            : thd::launch_norm_rope_fp32;
+  return launch(np, d.form, vec, sms, static_cast<cudaStream_t>(stream_ptr)) == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
 
 bool is_form(thd_attn_plan_t plan, thd_norm_rope_form_t form) {
