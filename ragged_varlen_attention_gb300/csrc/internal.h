@@ -346,6 +346,7 @@ struct PagedTablesParams {
   int32_t* free_begin_out;
   int64_t table_stride;
   int32_t batch, page_size, num_pages, max_pages, cap_rows, cap_free;
+  FastDiv by_page;
   uint32_t* status;
 };
 constexpr int kPagedMaxBatch = 8192;

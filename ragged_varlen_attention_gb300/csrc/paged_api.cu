@@ -231,6 +231,7 @@ thd_status_t thd_paged_tables(thd_attn_plan_t plan, const int32_t* seq_lens, con
   tp.table_stride = d.table_stride;
   tp.batch = d.batch; tp.page_size = d.page_size; tp.num_pages = d.num_pages; tp.max_pages = d.max_pages;
   tp.cap_rows = d.cap_rows; tp.cap_free = d.cap_free;
+  tp.by_page = thd::FastDiv(d.page_size);
   tp.status = static_cast<uint32_t*>(workspace);
   return thd::launch_paged_tables(tp, static_cast<cudaStream_t>(stream)) == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }

@@ -101,6 +101,12 @@ struct Cursor {
   }
 };
 
+// a / b below 2^31 of non-negative numbers; a 64-bit division, a few hundred cycles, only
+// where one is needed
+__device__ __forceinline__ int32_t quotient(int64_t a, int32_t b) {
+  return (a >> 32) == 0 ? (int32_t)((uint32_t)a / (uint32_t)b) : (int32_t)(a / b);
+}
+
 // The line's `total` chunks over the workers (warps): `each` of them, the first `extra`
 // workers one more.
 struct Line {
@@ -110,7 +116,7 @@ struct Line {
   // the worker that holds chunk t
   __device__ __forceinline__ int32_t holder(int64_t t) const {
     const int64_t big = (int64_t)extra * (each + 1);
-    return t < big ? (int32_t)(t / (each + 1)) : extra + (int32_t)((t - big) / each);
+    return t < big ? quotient(t, each + 1) : extra + quotient(t - big, each);
   }
 };
 
@@ -145,7 +151,7 @@ __device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC
   }
   line.total = total * segs;
   line.workers = (int32_t)min64((int64_t)gridDim.x * kWarps, max64(line.total, 1));
-  line.each = (int32_t)(line.total / line.workers);  // below 2^31 by the plan's bound
+  line.each = quotient(line.total, line.workers);  // below 2^31 by the plan's bound
   line.extra = (int32_t)(line.total - (int64_t)line.each * line.workers);
   // the request that each of the block's workers begins in
 #pragma unroll
@@ -170,7 +176,7 @@ __device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC
   cur.b = found_b[warp];
   cur.sp = span_of<KC>(p, cur.b);
   const int64_t rel = line.start(worker) - found_before[warp];  // below segs x chunks
-  cur.seg = (int)(rel / cur.sp.chunks);
+  cur.seg = quotient(rel, cur.sp.chunks);
   cur.chunk = (int)(rel - (int64_t)cur.seg * cur.sp.chunks);
   return (int)(line.start(worker + 1) - line.start(worker));
 }
@@ -332,21 +338,22 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   Cursor<kKeys> load = cur;
   int issued = 0;
   uint32_t load_stage = 0;
-  // the page of key lane % kKeys of the chunk at `load` (-1: none), looked up one step
-  // before it is used
-  int key_page = -1, key_row = 0;
+  // key lane % kKeys of the chunk at `load`: whether it is visible, and where it is, looked
+  // up one step before it is used
+  bool key_seen = false;
+  int64_t key_k = 0, key_v = 0;  // its rows' offsets in the caches
+  const bool same = p.k_page == p.v_page && p.k_tok == p.v_tok;
   auto look_up = [&]() {
-    key_page = -1;
+    key_seen = false;
     if (issued >= steps) return;
     const int key = load.sp.base + load.chunk * kKeys + (lane & (kKeys - 1));
     if (key >= load.sp.lo && key < load.sp.n) {
-      const int column = p.by_page.div(key);
-      key_row = key - column * p.page_size;
-      key_page = p.block_table[(int64_t)load.b * p.table_stride + column];
-      if (key_page < 0 || key_page >= p.num_pages) {
-        status |= THD_DEV_BAD_PAGE;
-        key_page = -1;
-      }
+      const int column = p.by_page.div(key), row = key - column * p.page_size;
+      const int page = p.block_table[(int64_t)load.b * p.table_stride + column];
+      key_seen = page >= 0 && page < p.num_pages;
+      if (!key_seen) status |= THD_DEV_BAD_PAGE;
+      key_k = page * p.k_page + row * p.k_tok;
+      key_v = same ? key_k : page * p.v_page + row * p.v_tok;
     }
   };
   constexpr uint32_t kAll = kKeys == 16 ? 0xffffu : 0xffffffffu;
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   const bool whole_pages = (p.page_size & 15) == 0 && p.d == D;
   auto issue = [&]() {
     if (issued < steps) {
-      const uint32_t seen = __ballot_sync(0xffffffffu, key_page >= 0) & kAll;
+      const uint32_t seen = __ballot_sync(0xffffffffu, key_seen) & kAll;
       if (lane == 0) sm.seen[warp][load_stage] = seen;
       const uint32_t dst = ring + load_stage * Smem::kStageBytes + row_in * kPitch + vec * 16;
       const int g = load.seg / per;
@@ -366,10 +373,10 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
       if (whole_pages && seen == kAll) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const int page = __shfl_sync(0xffffffffu, key_page, mt * 16);
-          const int in_page = __shfl_sync(0xffffffffu, key_row, mt * 16) + row_in;
-          const T* ks = kh + (int64_t)page * p.k_page + (int64_t)in_page * p.k_tok;
-          const T* vs = vh + (int64_t)page * p.v_page + (int64_t)in_page * p.v_tok;
+          const int64_t at_k = __shfl_sync(0xffffffffu, key_k, mt * 16);
+          const int64_t at_v = same ? at_k : __shfl_sync(0xffffffffu, key_v, mt * 16);
+          const T* ks = kh + at_k + row_in * p.k_tok;
+          const T* vs = vh + at_v + row_in * p.v_tok;
 #pragma unroll
           for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
             const uint32_t at = dst + (mt * 16 + i * kRowsAtOnce) * kPitch;
@@ -382,16 +389,13 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
       } else {
 #pragma unroll
         for (int i = 0; i < kKeys / kRowsAtOnce; ++i) {
-          const int page = __shfl_sync(0xffffffffu, key_page, i * kRowsAtOnce + row_in);
-          const int in_page = __shfl_sync(0xffffffffu, key_row, i * kRowsAtOnce + row_in);
-          const bool real = page >= 0 && vec_real;
+          const int row = i * kRowsAtOnce + row_in;
+          const int64_t at_k = __shfl_sync(0xffffffffu, key_k, row);
+          const int64_t at_v = same ? at_k : __shfl_sync(0xffffffffu, key_v, row);
+          const bool real = ((seen >> row) & 1) && vec_real;
           const uint32_t at = dst + i * kRowsAtOnce * kPitch;
-          const T* ks = static_cast<const T*>(p.k);
-          const T* vs = static_cast<const T*>(p.v);
-          if (real) {
-            ks = kh + (int64_t)page * p.k_page + (int64_t)in_page * p.k_tok;
-            vs = vh + (int64_t)page * p.v_page + (int64_t)in_page * p.v_tok;
-          }
+          const T* ks = real ? kh + at_k : static_cast<const T*>(p.k);
+          const T* vs = real ? vh + at_v : static_cast<const T*>(p.v);
           cp_async16(at, ks, real);
           cp_async16(at + kKeys * kPitch, vs, real);
         }
@@ -728,90 +732,122 @@ __global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParam
 }
 
 // ----------------------------------------------------------------- join kernel
-// Block (w, t): if worker w's range is the first to begin inside a segment, merge the
-// segment's pieces for 8 of its heads. The piece that begins the segment is slot
-// 2 (w - 1) + 1, the others are slots 2w, 2 (w + 1), ... Each warp takes every eighth piece
-// with all 8 heads (4 KB in flight at d = 128), then the warps' results are merged in order.
+// Block (x, h) looks at the records of 8 workers, a warp each, and merges the pieces of the
+// segments that they own for one head. The piece that begins the segment is slot
+// 2 (w - 1) + 1, the others are slots 2w, 2 (w + 1), ... Up to 8 pieces are the warp's own
+// work, more are shared by the block's warps (every eighth piece) and merged in warp order:
+// a long request alone leaves hundreds, and a warp would read them one latency after another.
 constexpr int kJoinWarps = 8;
+
+// The running result of a warp: base-2 maximum and sum, and the lane's elements.
+template <int D>
+struct Merged {
+  static constexpr int kPer = D / 32;
+  float top, sum, o[kPer];
+  __device__ __forceinline__ void clear() {
+    top = -INFINITY;
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] = 0.f;
+  }
+  __device__ __forceinline__ void add(float lse, float weight, const float (&x)[kPer]) {
+    const float now = fmaxf(top, lse), ref = now == -INFINITY ? 0.f : now;
+    const float f = ptx::ex2(top - ref), g = ptx::ex2(lse - ref);
+    top = now;
+    sum = sum * f + g * weight;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] = o[k] * f + g * x[k];
+  }
+  // pieces first, first + step, ... of worker w's segment
+  template <int HEADS>
+  __device__ __forceinline__ void read(const DecodeParams& p, int w, int h, int pieces, int first, int step) {
+    constexpr int kAtOnce = 4;
+    for (int i0 = first; i0 < pieces; i0 += kAtOnce * step) {
+      float lse[kAtOnce], x[kAtOnce][kPer];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int i = i0 + a * step;
+        lse[a] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) x[a][k] = 0.f;
+        if (i < pieces) {
+          const int64_t row = (int64_t)(i == 0 ? 2 * w - 1 : 2 * (w + i - 1)) * HEADS + h;
+          lse[a] = p.part_lse[row];
+          const float* src = p.part_o + row * D + (threadIdx.x & 31) * kPer;
+          if constexpr (kPer == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            x[a][0] = v.x; x[a][1] = v.y; x[a][2] = v.z; x[a][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            x[a][0] = v.x; x[a][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) add(lse[a], 1.f, x[a]);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void write(const DecodeParams& p, int b, int head) {
+    const bool dead = top == -INFINITY;
+    const float inv = dead ? 0.f : 1.f / sum;
+    const int lane = threadIdx.x & 31;
+    T* dst = static_cast<T*>(p.o) + (int64_t)b * p.o_tok + (int64_t)head * p.o_head;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (lane * kPer + k < p.d) dst[lane * kPer + k] = from_f<T>(o[k] * inv);
+    if (lane == 0 && p.stats)
+      p.stats[(int64_t)b * p.stats_tok + (int64_t)head * p.stats_head] = dead ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+};
+
 template <typename T, int D, int HEADS>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_decode_join_kernel(DecodeParams p) {
-  constexpr int kPer = D / 32;
-  __shared__ float part_o[kJoinWarps][8][D];
-  __shared__ float part_max[kJoinWarps][8], part_sum[kJoinWarps][8];
+  __shared__ float part_o[kJoinWarps][D];
+  __shared__ float part_max[kJoinWarps], part_sum[kJoinWarps];
+  __shared__ DecodeRec shared_rec[kJoinWarps];
   ptx::pdl_wait();
   ptx::pdl_release();
-  const int w0 = blockIdx.x;
-  const DecodeRec rec = p.recs[w0];
-  const int pieces = rec.pieces;
-  if (pieces == 0) return;
-  int head0;
-  const int h8 = blockIdx.y * 8;
-  const int heads = segment_heads<HEADS>(p, rec.seg, head0) - h8;
-  if (heads <= 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  float top[8], sum[8], acc[8][kPer];
-#pragma unroll
-  for (int h = 0; h < 8; ++h) {
-    top[h] = -INFINITY;
-    sum[h] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[h][k] = 0.f;
-  }
-  for (int i = warp; i < pieces; i += kJoinWarps) {
-    const int slot = i == 0 ? 2 * (w0 - 1) + 1 : 2 * (w0 + i - 1);
-    const int64_t row = (int64_t)slot * HEADS + h8;
-    float lse[8], o[8][kPer];
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      lse[h] = h < heads ? p.part_lse[row + h] : -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) o[h][k] = h < heads ? p.part_o[(row + h) * D + lane + 32 * k] : 0.f;
-    }
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      const float now = fmaxf(top[h], lse[h]), ref = now == -INFINITY ? 0.f : now;
-      const float f = ptx::ex2(top[h] - ref), g = ptx::ex2(lse[h] - ref);
-      top[h] = now;
-      sum[h] = sum[h] * f + g;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[h][k] = acc[h][k] * f + g * o[h][k];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, h = blockIdx.y;
+  const int w = blockIdx.x * kJoinWarps + warp;
+  const DecodeRec rec = p.recs[w];
+  const bool many = rec.pieces > kJoinWarps;
+  if (lane == 0) shared_rec[warp] = rec;
+  Merged<D> m;
+  if (rec.pieces > 0 && !many) {
+    int head0;
+    if (h < segment_heads<HEADS>(p, rec.seg, head0)) {
+      m.clear();
+      m.template read<HEADS>(p, w, h, rec.pieces, 0, 1);
+      m.template write<T>(p, rec.b, head0 + h);
     }
   }
+  if (!__syncthreads_or(many)) return;
+  for (int o = 0; o < kJoinWarps; ++o) {
+    const DecodeRec r = shared_rec[o];
+    int head0;
+    if (r.pieces <= kJoinWarps || h >= segment_heads<HEADS>(p, r.seg, head0)) continue;
+    m.clear();
+    m.template read<HEADS>(p, blockIdx.x * kJoinWarps + o, h, r.pieces, warp, kJoinWarps);
+    __syncthreads();  // the last segment's results have been read
 #pragma unroll
-  for (int h = 0; h < 8; ++h) {
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) part_o[warp][h][lane + 32 * k] = acc[h][k];
+    for (int k = 0; k < m.kPer; ++k) part_o[warp][lane * m.kPer + k] = m.o[k];
     if (lane == 0) {
-      part_max[warp][h] = top[h];
-      part_sum[warp][h] = sum[h];
+      part_max[warp] = m.top;
+      part_sum[warp] = m.sum;
     }
+    __syncthreads();
+    if (warp != 0) continue;
+    m.clear();
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+      float x[m.kPer];
+#pragma unroll
+      for (int k = 0; k < m.kPer; ++k) x[k] = part_o[i][lane * m.kPer + k];
+      m.add(part_max[i], part_sum[i], x);
+    }
+    m.template write<T>(p, r.b, head0 + h);
   }
-  __syncthreads();
-  static_assert(kJoinWarps == 8, "warp h finishes head h");
-  const int h = warp;
-  if (h >= heads) return;
-  float all = part_max[0][h];
-#pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) all = fmaxf(all, part_max[w][h]);
-  const bool dead = all == -INFINITY;
-  float l = 0.f, o[kPer];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) o[k] = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float f = dead ? 0.f : ptx::ex2(part_max[w][h] - all);
-    l += f * part_sum[w][h];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) o[k] += f * part_o[w][h][lane + 32 * k];
-  }
-  const float inv = dead ? 0.f : 1.f / l;
-  T* dst = static_cast<T*>(p.o) + (int64_t)rec.b * p.o_tok + (int64_t)(head0 + h8 + h) * p.o_head;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k)
-    if (lane + 32 * k < p.d) dst[lane + 32 * k] = from_f<T>(o[k] * inv);
-  if (lane == 0 && p.stats)
-    p.stats[(int64_t)rec.b * p.stats_tok + (int64_t)(head0 + h8 + h) * p.stats_head] =
-        dead ? -INFINITY : (all + log2f(l)) * kLn2;
 }
 
 template <typename T, int D, int NT>
@@ -822,14 +858,16 @@ cudaError_t launch_mma(const DecodeParams& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_overlapped(paged_decode_mma_kernel<T, D, NT>, ctas, kThreads, bytes, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(paged_decode_join_kernel<T, D, 8 * NT>, dim3(ctas * kWarps, NT), 32 * kJoinWarps, 0, stream, p);
+  return launch_overlapped(paged_decode_join_kernel<T, D, 8 * NT>, dim3(ctas * kWarps / kJoinWarps, 8 * NT),
+                           32 * kJoinWarps, 0, stream, p);
 }
 
 template <typename T, int D>
 cudaError_t launch_simt(const DecodeParams& p, int ctas, cudaStream_t stream) {
   const cudaError_t e = launch_overlapped(paged_decode_simt_kernel<T, D>, ctas, kThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(paged_decode_join_kernel<T, D, 8>, ctas * kWarps, 32 * kJoinWarps, 0, stream, p);
+  return launch_overlapped(paged_decode_join_kernel<T, D, 8>, dim3(ctas * kWarps / kJoinWarps, 8), 32 * kJoinWarps, 0,
+                           stream, p);
 }
 
 template <typename T, int D>
@@ -854,7 +892,7 @@ cudaError_t launch_type(const DecodeParams& p, bool mma, int ctas, cudaStream_t 
 
 cudaError_t launch_paged_decode(const DecodeParams& p, thd_dtype_t dtype, bool mma, int num_sms, cudaStream_t stream) {
   const int sms = num_sms < kMaxSmsForSizing ? num_sms : kMaxSmsForSizing;
-  const int ctas = sms * kDecodeCtasPerSm;
+  const int ctas = sms * kDecodeCtasPerSm;  // even: the join kernel takes 8 workers a block
   switch (dtype) {
     case THD_BF16: return launch_type<__nv_bfloat16>(p, mma, ctas, stream);
     case THD_FP16: return launch_type<__half>(p, mma, ctas, stream);

@@ -34,6 +34,11 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums) {
   return v + before;
 }
 
+// pages that n >= 0 tokens take
+__device__ __forceinline__ int32_t pages_of(const PagedTablesParams& p, int32_t n) {
+  return n > 0 ? p.by_page.div(n - 1) + 1 : 0;
+}
+
 struct Request {
   int32_t len, need;
   bool bad;
@@ -44,9 +49,7 @@ __device__ __forceinline__ Request request_of(const PagedTablesParams& p, int b)
   r.len = p.seq_lens[b];
   const int64_t after = (int64_t)r.len + (p.cu_new[b + 1] - p.cu_new[b]);
   r.bad = r.len < 0 || after > (int64_t)p.max_pages * p.page_size;
-  r.need = r.bad ? 0
-                 : (int32_t)((after + p.page_size - 1) / p.page_size -
-                             ((int64_t)r.len + p.page_size - 1) / p.page_size);
+  r.need = r.bad ? 0 : pages_of(p, (int32_t)after) - pages_of(p, r.len);
   return r;
 }
 
@@ -98,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(PagedTablesParam
       if (bad) {
         p.seq_lens_out[b] = p.seq_lens[b];
       } else {
-        const int64_t old = (len + p.page_size - 1) / p.page_size;
+        const int64_t old = pages_of(p, (int32_t)len);
         const int64_t after = len + (p.cu_new[b + 1] - p.cu_new[b]);
         p.seq_lens_out[b] = (int32_t)min64(after, (old + got) * p.page_size);
       }
@@ -136,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(PagedTablesParam
       if (first < 0) continue;
       const int len = p.seq_lens[b];
       const int pos = len + (row - p.cu_new[b]);
-      const int column = pos / p.page_size, in_page = pos - column * p.page_size;
-      const int old = (int)(((int64_t)len + p.page_size - 1) / p.page_size);
+      const int column = p.by_page.div(pos), in_page = pos - column * p.page_size;
+      const int old = pages_of(p, len);
       position[i] = pos;
       int page;
       if (column < old) {
