@@ -48,6 +48,26 @@ __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Sums N values over the group's lanes at once: each step hands half of the values to the
+// other half of the lanes, so that N + log2(G/N) shuffles do what N log2(G) would. Lane l of
+// the group returns the sum of value l / (G / N).
+template <int G, int N>
+__device__ __forceinline__ float sum_each(float (&v)[N]) {
+  int bit = G / 2;
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1, bit >>= 1) {
+    const bool upper = threadIdx.x & bit;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = upper ? v[i + n] : v[i], give = upper ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+    }
+  }
+#pragma unroll
+  for (; bit > 0; bit >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+  return v[0];
+}
+
 // A lane's 8 elements of a row as loaded: 4 from e0, 4 from e1.
 template <typename T>
 struct Raw {
@@ -193,6 +213,13 @@ __device__ __forceinline__ bool cache_row(const NormRopeParams& p, int which, in
   return true;
 }
 
+// Strides of a view: the row of token t and head h is base + t tok + h head.
+struct Where {
+  int64_t tok, head;
+  template <typename P>
+  __device__ __forceinline__ P* at(P* base, int t, int h) const { return base + t * tok + h * head; }
+};
+
 // One tensor's rows (WHICH: 0 Q, 1 K, 2 V) among the launch's units. `u` is the warp's first
 // unit counted from the tensor's; on return, counted from the next tensor's. ONE: the heads
 // are a multiple of a unit's rows, so that a unit is of one token, with one position and one
@@ -228,27 +255,44 @@ __device__ __forceinline__ void rows_of(const NormRopeParams& p, int64_t& u, Eig
     }
   }
 
+  // the lane's rows of a unit (ONE: a constant stride apart, and a whole number of units)
   struct Unit {
     Raw<T> x[kUnroll], g[kBack ? kUnroll : 1];
     int pos[ONE ? 1 : kUnroll];
   };
+  const Where in = {p.in_tok[WHICH], p.in_head[WHICH]};
+  const Where gin = {p.in_tok[kBack ? 2 + WHICH : 0], p.in_head[kBack ? 2 + WHICH : 0]};
+  const Where out = {p.out_tok[WHICH], p.out_head[WHICH]};
+  const T* const x_base = static_cast<const T*>(p.in[WHICH]);
+  const T* const g_base = static_cast<const T*>(p.in[kBack ? 2 + WHICH : 0]);
   const auto load = [&](Unit& n, int64_t unit) {
-    const int row0 = (int)unit * kRows + sub;
+    const int first = (int)unit * kRows;
+    const T *x = nullptr, *g = nullptr;
+    if (ONE) {
+      const int t = by_heads.div(first), h = first - t * by_heads.d + sub;
+      n.pos[0] = p.positions[t];
+      x = in.at(x_base, t, h);
+      if constexpr (kBack) g = gin.at(g_base, t, h);
+    }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int row = row0 + i * kAtOnce;
-      const int t = by_heads.div(ONE ? (int)unit * kRows : min(row, rows - 1)), h = row - t * by_heads.d;
-      if (i == 0 || !ONE) n.pos[ONE ? 0 : i] = p.positions[t];
-      if (active && row < rows) {
-        n.x[i].load(static_cast<const T*>(p.in[WHICH]) + (int64_t)t * p.in_tok[WHICH] + (int64_t)h * p.in_head[WHICH], e0,
-                    e1);
-        if constexpr (kBack)
-          n.g[i].load(static_cast<const T*>(p.in[2 + WHICH]) + (int64_t)t * p.in_tok[2 + WHICH] +
-                          (int64_t)h * p.in_head[2 + WHICH],
-                      e0, e1);
+      const int row = first + sub + i * kAtOnce;
+      if (!ONE) {
+        const int t = by_heads.div(min(row, rows - 1)), h = row - t * by_heads.d;
+        n.pos[i] = p.positions[t];
+        x = in.at(x_base, t, h);
+        if constexpr (kBack) g = gin.at(g_base, t, h);
+      }
+      if (active && (ONE || row < rows)) {
+        n.x[i].load(x, e0, e1);
+        if constexpr (kBack) n.g[i].load(g, e0, e1);
       } else {
         n.x[i].zero();
         if constexpr (kBack) n.g[i].zero();
+      }
+      if (ONE) {
+        x += kAtOnce * in.head;
+        if constexpr (kBack) g += kAtOnce * gin.head;
       }
     }
   };
@@ -257,65 +301,98 @@ __device__ __forceinline__ void rows_of(const NormRopeParams& p, int64_t& u, Eig
   for (; u < units; u += stride) {
     Unit now = next;
     if (u + stride < units) load(next, u + stride);
-    const int row0 = (int)u * kRows + sub;
+    const int first = (int)u * kRows;
     // where the rows go, and the angles: all rows' loads before the first is used
     T* dst[kUnroll];
     bool write[kUnroll], skip[kUnroll];
     Angles angles[ONE || WHICH == 2 ? 1 : kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int row = row0 + i * kAtOnce;
-      const int t = by_heads.div(ONE ? (int)u * kRows : min(row, rows - 1)), h = row - t * by_heads.d;
-      const int pos = now.pos[ONE ? 0 : i];
+      if (ONE && i > 0) {
+        skip[i] = skip[0];
+        write[i] = write[0];
+        dst[i] = dst[i - 1] + kAtOnce * out.head;
+        continue;
+      }
+      const int row = first + sub + i * kAtOnce;
+      const int t = by_heads.div(ONE ? first : min(row, rows - 1)), h = row - t * by_heads.d;
+      const int pos = now.pos[i];
       skip[i] = pos < 0 || pos >= p.max_pos;
       if (pos >= p.max_pos) status |= THD_DEV_BAD_POSITION;
       if constexpr (kCached) {
         const int slot = p.slot_map[t];
         if (slot >= p.num_slots) status |= THD_DEV_BAD_PAGE;
         write[i] = !skip[i] && cache_row(p, WHICH, slot, dst[i]);
+        dst[i] += (int64_t)h * out.head;
       } else {
-        dst[i] = static_cast<T*>(p.out[WHICH]) + (int64_t)t * p.out_tok[WHICH];
+        dst[i] = out.at(static_cast<T*>(p.out[WHICH]), t, h);
         write[i] = !skip[i] || p.zero_skipped;
       }
-      write[i] = write[i] && active && row < rows;
-      dst[i] += (int64_t)h * p.out_head[WHICH];
+      write[i] = write[i] && active && (ONE || row < rows);
       if constexpr (WHICH < 2)
-        if ((i == 0 || !ONE) && rotated && !skip[i])
-          angles[ONE ? 0 : i].load(p.cos_sin + (int64_t)pos * p.rot + 4 * item, p.rot / 2);
+        if (rotated && !skip[i]) angles[i].load(p.cos_sin + (int64_t)pos * p.rot + 4 * item, p.rot / 2);
     }
+    if constexpr (WHICH == 2) {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      Raw<T>& raw = now.x[i];
-      if constexpr (WHICH < 2) {
-        Eight x;
-        x.get<T, ADJ>(raw);
-        const float r = rsqrtf(group_sum<G>(dot(x, x)) * inv_d + p.eps);
-        if constexpr (!kBack) {
+      for (int i = 0; i < kUnroll; ++i)
+        if (write[i]) now.x[i].store(dst[i], e0, e1);
+    } else if constexpr (!kBack) {
+      Eight x[kUnroll];
+      float ss[kUnroll];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x.v[k] = ptx::f2_mul(ptx::f2_mul(x.v[k], both(r)), w.v[k]);
-          if (rotated && !skip[i]) angles[ONE ? 0 : i].template turn<false>(x);
-        } else {
-          Eight g, a;
-          g.get<T, ADJ>(now.g[i]);
-          if (rotated && !skip[i]) angles[ONE ? 0 : i].template turn<true>(g);
+      for (int i = 0; i < kUnroll; ++i) {
+        x[i].template get<T, ADJ>(now.x[i]);
+        ss[i] = dot(x[i], x[i]);
+      }
+      const float r_mine = rsqrtf(sum_each<G, kUnroll>(ss) * inv_d + p.eps);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) a.v[k] = ptx::f2_mul(g.v[k], w.v[k]);
-          const float mean = group_sum<G>(dot(a, x)) * r * inv_d;
-          const bool counts = !skip[i] && row0 + i * kAtOnce < rows;
+      for (int i = 0; i < kUnroll; ++i) {
+        const float r = __shfl_sync(0xffffffffu, r_mine, i * (G / kUnroll), G);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i].v[k] = ptx::f2_mul(ptx::f2_mul(x[i].v[k], both(r)), w.v[k]);
+        if (rotated && !skip[i]) angles[ONE ? 0 : i].template turn<false>(x[i]);
+        Raw<T> raw;
+        if (skip[i]) raw.zero();
+        else x[i].template put<T, ADJ>(raw);
+        if (write[i]) raw.store(dst[i], e0, e1);
+      }
+    } else {
+      // two rows at a time: dx = r a + c x with a = g w, c = -r^3 <a, x> / d
+#pragma unroll
+      for (int i = 0; i < kUnroll; i += 2) {
+        Eight x[2], g[2], a[2];
+        float sums[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x[j].template get<T, ADJ>(now.x[i + j]);
+          g[j].template get<T, ADJ>(now.g[i + j]);
+          if (rotated && !skip[i + j]) angles[ONE ? 0 : i + j].template turn<true>(g[j]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) a[j].v[k] = ptx::f2_mul(g[j].v[k], w.v[k]);
+          sums[j] = dot(x[j], x[j]);
+          sums[2 + j] = dot(a[j], x[j]);
+        }
+        const float mine = sum_each<G, 4>(sums), other = __shfl_xor_sync(0xffffffffu, mine, G / 2);
+        const bool upper = threadIdx.x & (G / 2);
+        const float r_mine = rsqrtf((upper ? other : mine) * inv_d + p.eps);
+        const float c_mine = -(r_mine * r_mine * r_mine) * ((upper ? mine : other) * inv_d);
+        const float give = upper ? c_mine : r_mine;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float r = __shfl_sync(0xffffffffu, give, j * (G / 4), G);
+          const float c = __shfl_sync(0xffffffffu, give, (2 + j) * (G / 4), G);
+          const bool counts = !skip[i + j] && (ONE || first + sub + (i + j) * kAtOnce < rows);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint64_t xh = ptx::f2_mul(x.v[k], both(r));
-            if (counts) acc.v[k] = ptx::f2_fma(g.v[k], xh, acc.v[k]);
-            x.v[k] = ptx::f2_mul(ptx::f2_fma(xh, both(-mean), a.v[k]), both(r));
+            if (counts) acc.v[k] = ptx::f2_fma(g[j].v[k], ptx::f2_mul(x[j].v[k], both(r)), acc.v[k]);
+            x[j].v[k] = ptx::f2_fma(x[j].v[k], both(c), ptx::f2_mul(a[j].v[k], both(r)));
           }
-        }
-        if (skip[i]) {
-          raw.zero();
-        } else {
-          x.put<T, ADJ>(raw);
+          Raw<T> raw;
+          if (skip[i + j]) raw.zero();
+          else x[j].template put<T, ADJ>(raw);
+          if (write[i + j]) raw.store(dst[i + j], e0, e1);
         }
       }
-      if (write[i]) raw.store(dst[i], e0, e1);
     }
   }
   u -= units;
