@@ -179,7 +179,9 @@ __device__ __forceinline__ float dot(const Eight& x, const Eight& y) {
 struct Angles {
   uint64_t cos[2], sin[2], neg[2];
   __device__ __forceinline__ void load(const float* row, int half) {
-    const float4 c = *reinterpret_cast<const float4*>(row), s = *reinterpret_cast<const float4*>(row + half);
+    set(*reinterpret_cast<const float4*>(row), *reinterpret_cast<const float4*>(row + half));
+  }
+  __device__ __forceinline__ void set(const float4& c, const float4& s) {
     cos[0] = ptx::f2_pack(c.x, c.y); cos[1] = ptx::f2_pack(c.z, c.w);
     sin[0] = ptx::f2_pack(s.x, s.y); sin[1] = ptx::f2_pack(s.z, s.w);
     neg[0] = ptx::f2_pack(-s.x, -s.y); neg[1] = ptx::f2_pack(-s.z, -s.w);
@@ -270,7 +272,7 @@ __device__ __forceinline__ void rows_of(const NormRopeParams& p, int64_t& u, Eig
     const T *x = nullptr, *g = nullptr;
     if (ONE) {
       const int t = by_heads.div(first), h = first - t * by_heads.d + sub;
-      n.pos[0] = p.positions[t];
+      if (!kBack) n.pos[0] = p.positions[t];
       x = in.at(x_base, t, h);
       if constexpr (kBack) g = gin.at(g_base, t, h);
     }
@@ -296,16 +298,45 @@ __device__ __forceinline__ void rows_of(const NormRopeParams& p, int64_t& u, Eig
       }
     }
   };
+  // Backward and ONE: the next unit's row of the table is in flight too, by a position that was
+  // loaded a unit earlier still (the rotation is the first thing done to dz: without this a warp
+  // waited for the table for 1700 of the 4300 cycles of a unit).
+  constexpr bool kAhead = kBack && ONE;
+  float4 next_cos, next_sin;
+  int pos_after = -1;  // of the unit after the next
+  const auto load_angles = [&](int pos) {
+    if (rotated && pos >= 0 && pos < p.max_pos) {
+      const float* row = p.cos_sin + (int64_t)pos * p.rot + 4 * item;
+      next_cos = *reinterpret_cast<const float4*>(row);
+      next_sin = *reinterpret_cast<const float4*>(row + p.rot / 2);
+    }
+  };
+  const auto position = [&](int64_t unit) { return unit < units ? p.positions[by_heads.div((int)unit * kRows)] : -1; };
   Unit next;
-  if (u < units) load(next, u);
+  if (u < units) {
+    load(next, u);
+    if constexpr (kAhead) {
+      next.pos[0] = position(u);
+      load_angles(next.pos[0]);
+      pos_after = position(u + stride);
+    }
+  }
   for (; u < units; u += stride) {
     Unit now = next;
-    if (u + stride < units) load(next, u + stride);
+    Angles angles[ONE || WHICH == 2 ? 1 : kUnroll];
+    if constexpr (kAhead) angles[0].set(next_cos, next_sin);
+    if (u + stride < units) {
+      load(next, u + stride);
+      if constexpr (kAhead) {
+        next.pos[0] = pos_after;
+        load_angles(pos_after);
+        pos_after = position(u + 2 * stride);
+      }
+    }
     const int first = (int)u * kRows;
     // where the rows go, and the angles: all rows' loads before the first is used
     T* dst[kUnroll];
     bool write[kUnroll], skip[kUnroll];
-    Angles angles[ONE || WHICH == 2 ? 1 : kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       if (ONE && i > 0) {
@@ -329,7 +360,7 @@ __device__ __forceinline__ void rows_of(const NormRopeParams& p, int64_t& u, Eig
         write[i] = !skip[i] || p.zero_skipped;
       }
       write[i] = write[i] && active && (ONE || row < rows);
-      if constexpr (WHICH < 2)
+      if constexpr (WHICH < 2 && !kAhead)
         if (rotated && !skip[i]) angles[i].load(p.cos_sin + (int64_t)pos * p.rot + 4 * item, p.rot / 2);
     }
     if constexpr (WHICH == 2) {
