@@ -375,6 +375,7 @@ struct DecodeParams {
   int32_t batch, h_q, h_kv, d, group;
   int32_t page_size, num_pages, max_pages;
   FastDiv by_page;
+  int32_t aligned;          // cache rows are whole 16-byte pieces (SIMT kernel)
   float scale_log2;
   uint32_t* status;
   DecodeRec* recs;          // [workers]
@@ -382,11 +383,13 @@ struct DecodeParams {
   float* part_lse;          // [2 workers][heads of a segment] base-2 log-sum-exp
 };
 constexpr int kDecodeCtasPerSm = 2;
-constexpr int kDecodeMinChunk = 16;   // keys of the smallest unit of the schedule
+constexpr int kDecodeMinChunk = 8;    // keys of the smallest unit of the schedule
 constexpr int kDecodeMaxCtas = kDecodeCtasPerSm * kMaxSmsForSizing;
 constexpr int kDecodeMaxWorkers = 4 * kDecodeMaxCtas;
 // query heads a segment holds (a kv head whose group is larger has several segments)
-constexpr int decode_seg_heads(int group, bool mma) { return !mma || group <= 8 ? 8 : group <= 16 ? 16 : 32; }
+constexpr int decode_seg_heads(int group, bool mma) {
+  return !mma ? (group <= 4 ? 4 : 8) : group <= 8 ? 8 : group <= 16 ? 16 : 32;
+}
 constexpr int decode_pad_d(int d) { return d <= 64 ? 64 : 128; }
 cudaError_t launch_paged_decode(const DecodeParams& p, thd_dtype_t dtype, bool mma, int num_sms, cudaStream_t stream);
 

@@ -325,6 +325,11 @@ thd_status_t thd_paged_decode(thd_attn_plan_t plan, const void* q, const void* k
   dp.batch = d.batch; dp.h_q = d.h_q; dp.h_kv = d.h_kv; dp.d = d.d; dp.group = d.h_q / d.h_kv;
   dp.page_size = d.page_size; dp.num_pages = d.num_pages; dp.max_pages = d.max_pages;
   dp.by_page = thd::FastDiv(d.page_size);
+  const int64_t eb = plan->elem_bytes;
+  dp.aligned = aligned(k_cache, 16) && aligned(v_cache, 16) && d.d * eb % 16 == 0;
+  for (int i = 1; i < 3; ++i)
+    dp.aligned = dp.aligned && d.stride_tok[i] * eb % 16 == 0 && d.stride_head[i] * eb % 16 == 0 &&
+                 d.stride_page[i] * eb % 16 == 0;
   dp.scale_log2 = plan->scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
   dp.status = reinterpret_cast<uint32_t*>(ws);

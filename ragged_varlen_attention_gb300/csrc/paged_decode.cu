@@ -31,7 +31,8 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // keys of a chunk: half of the rows that a warp's stage holds (K and V) with d = 128, all
 // of them with d = 64, so that a stage is 8 KB either way
 constexpr int chunk_keys(int pad_d) { return pad_d == 128 ? 16 : 32; }
-static_assert(chunk_keys(128) >= kDecodeMinChunk, "the plan's bound counts these chunks");
+constexpr int simt_chunk_keys(int pad_d) { return pad_d == 128 ? 8 : 16; }  // 8 KB of float32
+static_assert(simt_chunk_keys(128) >= kDecodeMinChunk, "the plan's bound counts these chunks");
 static_assert(kWarps * kDecodeMaxCtas == kDecodeMaxWorkers, "the workspace is sized for these workers");
 
 template <typename T>
@@ -224,7 +225,20 @@ __device__ __forceinline__ int piece_slot(int worker, int first, int last, int c
   return first > 0 ? 2 * worker : last + 1 < chunks ? 2 * worker + 1 : -1;
 }
 
-// ------------------------------------------------------------- matrix pieces
+// --------------------------------------------------- copies and matrix pieces
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes of zeros when not `real` (src is not read then)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  const int bytes = real ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -298,20 +312,6 @@ struct MmaSmem {
   unsigned char ring[kWarps][kStages][kStageBytes];
   uint32_t seen[kWarps][kStages];  // bit r: key r of the stage is visible
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// 16 bytes of zeros when not `real` (src is not read then)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  const int bytes = real ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_kernel(DecodeParams p) {
@@ -588,91 +588,165 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
 }
 
 // --------------------------------------------------------------- SIMT kernel
-// float32 caches, and any d <= 128 and alignment: the same schedule, a warp's 16 keys
-// taken 4 at a time with the head's elements spread over the lanes.
+// float32 caches, and any d <= 128 and alignment: the same schedule and ring of stages,
+// products by packed fma. A lane holds D / 32 consecutive elements of the HB query rows and of
+// their outputs. NK = 32 / HB keys at a time: each lane multiplies its elements for all 32
+// (head, key) pairs, the 32 sums over the lanes are folded in half at each of five shuffles
+// until lane h NK + j has the score of head h and key j, and its weight goes to all lanes
+// through shared memory. About 85 instructions a key with 8 heads, 45 with 4, of the 170 that
+// an SM issues while its share of the bandwidth brings a key (1 KB at d = 128).
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParams p) {
-  constexpr int kHeads = 8;
-  constexpr int kPer = D / 32;  // elements of a lane: e = lane + 32 i
-  constexpr int kChunk = 16;
-  constexpr int kKeys = 4;
-  const int lane = threadIdx.x & 31;
-  const int worker = blockIdx.x * kWarps + threadIdx.x / 32;
-  const int per = (p.group + kHeads - 1) / kHeads;
+struct SimtSmem {
+  static constexpr int kKeys = simt_chunk_keys(D);
+  static constexpr int kStages = 3;
+  T ring[kWarps][kStages][2 * kKeys][D];  // K rows, then V rows
+  float2 weight[kWarps][32];
+  uint32_t seen[kWarps][kStages];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void read_row(float (&f)[N], const T* row) {
+  if constexpr (sizeof(T) == 4 && N == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(row);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  } else if constexpr (sizeof(T) == 4) {
+    const float2 v = *reinterpret_cast<const float2*>(row);
+    f[0] = v.x; f[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_f(row[i]);
+  }
+}
+
+template <typename T, int D, int HB>
+__global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_simt_kernel(DecodeParams p) {
+  using Smem = SimtSmem<T, D>;
+  constexpr int kKeys = Smem::kKeys, kStages = Smem::kStages;
+  constexpr int kPer = D / 32, kPairs = kPer / 2;
+  constexpr int NK = 32 / HB;
+  extern __shared__ __align__(128) unsigned char raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int worker = blockIdx.x * kWarps + warp;
+  const int per = (p.group + HB - 1) / HB;
   const int segs = p.h_kv * per;
   ptx::pdl_wait();
   ptx::pdl_release();
   uint32_t status = 0;
-  Cursor<kChunk> cur;
+  Cursor<kKeys> cur;
   Line line;
-  const int steps = locate<kChunk>(p, segs, cur, line, status);
-  write_record<kChunk>(p, line, cur, steps);
+  const int steps = locate<kKeys>(p, segs, cur, line, status);
+
+  Cursor<kKeys> load = cur;
+  int issued = 0, load_stage = 0;
+  bool key_seen = false;
+  int64_t key_k = 0, key_v = 0;
+  auto look_up = [&]() {  // as in the matrix kernel
+    key_seen = false;
+    if (issued >= steps) return;
+    const int key = load.sp.base + load.chunk * kKeys + (lane & (kKeys - 1));
+    if (key >= load.sp.lo && key < load.sp.n) {
+      const int column = p.by_page.div(key), row = key - column * p.page_size;
+      const int page = p.block_table[(int64_t)load.b * p.table_stride + column];
+      key_seen = page >= 0 && page < p.num_pages;
+      if (!key_seen) status |= THD_DEV_BAD_PAGE;
+      key_k = page * p.k_page + row * p.k_tok;
+      key_v = page * p.v_page + row * p.v_tok;
+    }
+  };
+  constexpr int kVecs = D * (int)sizeof(T) / 16, kRowsAtOnce = kVecs >= 32 ? 1 : 32 / kVecs;
+  auto issue = [&]() {
+    if (issued < steps) {
+      const uint32_t seen = __ballot_sync(0xffffffffu, key_seen) & ((1u << kKeys) - 1);
+      if (lane == 0) sm.seen[warp][load_stage] = seen;
+      const int g = load.seg / per;
+      const T* kh = static_cast<const T*>(p.k) + (int64_t)g * p.k_head;
+      const T* vh = static_cast<const T*>(p.v) + (int64_t)g * p.v_head;
+      T(*rows)[D] = sm.ring[warp][load_stage];
+      if (p.aligned) {
+        const int vec = lane % kVecs * (16 / (int)sizeof(T)), row_in = lane / kVecs;
+#pragma unroll
+        for (int i = 0; i < kKeys / kRowsAtOnce; ++i) {
+          const int row = i * kRowsAtOnce + row_in;
+          const int64_t at_k = __shfl_sync(0xffffffffu, key_k, row), at_v = __shfl_sync(0xffffffffu, key_v, row);
+          const bool real = ((seen >> row) & 1) && vec < p.d;
+          cp_async16(ptx::smem_u32(&rows[row][vec]), real ? kh + at_k + vec : static_cast<const T*>(p.k), real);
+          cp_async16(ptx::smem_u32(&rows[kKeys + row][vec]), real ? vh + at_v + vec : static_cast<const T*>(p.v), real);
+        }
+      } else {
+        for (int row = 0; row < kKeys; ++row) {
+          const int64_t at_k = __shfl_sync(0xffffffffu, key_k, row), at_v = __shfl_sync(0xffffffffu, key_v, row);
+#pragma unroll
+          for (int e = lane; e < D; e += 32) {
+            const bool real = ((seen >> row) & 1) && e < p.d;
+            rows[row][e] = real ? kh[at_k + e] : from_f<T>(0.f);
+            rows[kKeys + row][e] = real ? vh[at_v + e] : from_f<T>(0.f);
+          }
+        }
+      }
+      ++issued;
+      load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
+      load.advance(p, segs, issued < steps);
+      look_up();
+    }
+    cp_commit();
+  };
+  look_up();
+  for (int i = 0; i < kStages - 1; ++i) issue();
+  write_record<kKeys>(p, line, cur, steps);
   write_empty<T>(p);
 
-  float q[8][kPer], acc[8][kPer], top[8], sum[8];
-  int head0 = 0, heads = 0, first = 0;
+  uint64_t q[HB][kPairs], acc[HB][kPairs];
+  float top = 0.f, sum = 0.f;  // of head lane / NK (the sum: of this lane's keys)
+  int head0 = 0, heads = 0, first = 0, stage = 0;
   bool fresh = true;
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
       first = cur.chunk;
-      heads = segment_heads<kHeads>(p, cur.seg, head0);
+      heads = segment_heads<HB>(p, cur.seg, head0);
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
+      for (int h = 0; h < HB; ++h) {
         const T* row = static_cast<const T*>(p.q) + (int64_t)cur.b * p.q_tok + (int64_t)(head0 + h) * p.q_head;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          q[h][i] = h < heads && lane + 32 * i < p.d ? to_f(row[lane + 32 * i]) * p.scale_log2 : 0.f;
-          acc[h][i] = 0.f;
-        }
-        top[h] = -INFINITY;
-        sum[h] = 0.f;
-      }
-    }
-    const int g = cur.seg / per;
-    const T* kh = static_cast<const T*>(p.k) + (int64_t)g * p.k_head;
-    const T* vh = static_cast<const T*>(p.v) + (int64_t)g * p.v_head;
-    int page = -1, in_page = 0;
-    {
-      const int key = cur.sp.base + cur.chunk * kChunk + (lane & (kChunk - 1));
-      if (key >= cur.sp.lo && key < cur.sp.n) {
-        const int column = p.by_page.div(key);
-        in_page = key - column * p.page_size;
-        page = p.block_table[(int64_t)cur.b * p.table_stride + column];
-        if (page < 0 || page >= p.num_pages) {
-          status |= THD_DEV_BAD_PAGE;
-          page = -1;
-        }
-      }
-    }
-    const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
-    for (int k0 = 0; k0 < kChunk; k0 += kKeys) {
-      if (((seen >> k0) & ((1u << kKeys) - 1)) == 0) continue;
-      float kv[kKeys][kPer], vv[kKeys][kPer];
+        for (int i = 0; i < kPairs; ++i) {
+          float v[2];
 #pragma unroll
-      for (int j = 0; j < kKeys; ++j) {
-        const int pg = __shfl_sync(0xffffffffu, page, k0 + j);
-        const int64_t ip = __shfl_sync(0xffffffffu, in_page, k0 + j);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int e = lane + 32 * i;
-          const bool real = pg >= 0 && e < p.d;
-          kv[j][i] = real ? to_f(kh[(int64_t)pg * p.k_page + ip * p.k_tok + e]) : 0.f;
-          vv[j][i] = real ? to_f(vh[(int64_t)pg * p.v_page + ip * p.v_tok + e]) : 0.f;
+          for (int j = 0; j < 2; ++j) {
+            const int e = lane * kPer + 2 * i + j;
+            v[j] = h < heads && e < p.d ? to_f(row[e]) * p.scale_log2 : 0.f;
+          }
+          q[h][i] = ptx::f2_pack(v[0], v[1]);
+          acc[h][i] = 0;
         }
       }
-      // lane 4 h + j ends with the score of head h and key j: 32 sums over the lanes,
-      // folded in half at each of five shuffles
+      top = -INFINITY;
+      sum = 0.f;
+    }
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    const uint32_t seen = sm.seen[warp][stage];
+    const T(*rows)[D] = sm.ring[warp][stage];
+#pragma unroll
+    for (int k0 = 0; k0 < kKeys; k0 += NK) {
+      if (((seen >> k0) & ((1u << NK) - 1)) == 0) continue;
       float v[32];
 #pragma unroll
-      for (int h = 0; h < 8; ++h)
+      for (int j = 0; j < NK; ++j) {
+        float f[kPer];
+        read_row(f, &rows[k0 + j][lane * kPer]);
+        uint64_t kk[kPairs];
 #pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-          float a = 0.f;
+        for (int i = 0; i < kPairs; ++i) kk[i] = ptx::f2_pack(f[2 * i], f[2 * i + 1]);
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) a += q[h][i] * kv[j][i];
-          v[h * kKeys + j] = a;
+        for (int h = 0; h < HB; ++h) {
+          uint64_t a = ptx::f2_mul(q[h][0], kk[0]);
+          if (kPairs == 2) a = ptx::f2_fma(q[h][kPairs - 1], kk[kPairs - 1], a);
+          float lo, hi;
+          ptx::f2_unpack(a, lo, hi);
+          v[h * NK + j] = lo + hi;
         }
+      }
 #pragma unroll
       for (int bit = 16; bit > 0; bit >>= 1) {
         const bool upper = lane & bit;
@@ -682,52 +756,82 @@ __global__ void __launch_bounds__(kThreads) paged_decode_simt_kernel(DecodeParam
           v[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
         }
       }
-      const bool visible = (seen >> (k0 + lane % kKeys)) & 1;
-      const float score = visible ? v[0] : -INFINITY;
-      float m = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const float score = (seen >> (k0 + lane % NK)) & 1 ? v[0] : -INFINITY;
+      float m = score;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        const float now = fmaxf(top[h], __shfl_sync(0xffffffffu, m, h * kKeys));
-        const float ref = now == -INFINITY ? 0.f : now;
-        const float f = exp2f(top[h] - ref);
-        top[h] = now;
-        sum[h] *= f;
+      for (int bit = 1; bit < NK; bit <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, bit));
+      m = fmaxf(m, top);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float scale = ptx::ex2(top - ref);
+      if (__any_sync(0xffffffffu, m != top)) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[h][i] *= f;
+        for (int h = 0; h < HB; ++h) {
+          const float f = __shfl_sync(0xffffffffu, scale, h * NK);
 #pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-          const float e = exp2f(__shfl_sync(0xffffffffu, score, h * kKeys + j) - ref);
-          sum[h] += e;
+          for (int i = 0; i < kPairs; ++i) acc[h][i] = ptx::f2_mul(acc[h][i], ptx::f2_pack(f, f));
+        }
+      }
+      top = m;
+      const float weight = ptx::ex2(score - ref);
+      sum = sum * scale + weight;
+      __syncwarp();
+      sm.weight[warp][lane] = make_float2(weight, weight);
+      __syncwarp();
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) acc[h][i] += e * vv[j][i];
+      for (int j = 0; j < NK; ++j) {
+        float f[kPer];
+        read_row(f, &rows[kKeys + k0 + j][lane * kPer]);
+        uint64_t vv[kPairs];
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) vv[i] = ptx::f2_pack(f[2 * i], f[2 * i + 1]);
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          const uint64_t w = *reinterpret_cast<const uint64_t*>(&sm.weight[warp][h * NK + j]);
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) acc[h][i] = ptx::f2_fma(w, vv[i], acc[h][i]);
         }
       }
     }
+    __syncwarp();  // the stage is read by every lane before it is filled again
+    issue();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+
     if (cur.chunk + 1 == cur.sp.chunks || step + 1 == steps) {
       const int slot = piece_slot(worker, first, cur.chunk, cur.sp.chunks);
+      float all = sum;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
+      for (int bit = 1; bit < NK; bit <<= 1) all += __shfl_xor_sync(0xffffffffu, all, bit);
+      const bool dead = top == -INFINITY;
+      const float inv_mine = dead ? 0.f : 1.f / all;
+      const float lse2 = dead ? -INFINITY : top + log2f(all);
+      const int mine = lane / NK;
+      if (lane % NK == 0 && mine < heads) {
+        if (slot >= 0) p.part_lse[(int64_t)slot * HB + mine] = lse2;
+        else if (p.stats) p.stats[(int64_t)cur.b * p.stats_tok + (int64_t)(head0 + mine) * p.stats_head] = lse2 * kLn2;
+      }
+#pragma unroll
+      for (int h = 0; h < HB; ++h) {
+        const float inv = __shfl_sync(0xffffffffu, inv_mine, h * NK);
         if (h >= heads) break;
-        const bool dead = top[h] == -INFINITY;
-        const float inv = dead ? 0.f : 1.f / sum[h];
-        const float lse2 = dead ? -INFINITY : top[h] + log2f(sum[h]);
         T* row = static_cast<T*>(p.o) + (int64_t)cur.b * p.o_tok + (int64_t)(head0 + h) * p.o_head;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int e = lane + 32 * i;
-          if (slot >= 0) p.part_o[((int64_t)slot * kHeads + h) * D + e] = acc[h][i] * inv;
-          else if (e < p.d) row[e] = from_f<T>(acc[h][i] * inv);
-        }
-        if (lane == 0) {
-          if (slot >= 0) p.part_lse[(int64_t)slot * kHeads + h] = lse2;
-          else if (p.stats) p.stats[(int64_t)cur.b * p.stats_tok + (int64_t)(head0 + h) * p.stats_head] = lse2 * kLn2;
+        for (int i = 0; i < kPairs; ++i) {
+          float v[2];
+          ptx::f2_unpack(acc[h][i], v[0], v[1]);
+          const int e = lane * kPer + 2 * i;
+          if (slot >= 0) {
+            *reinterpret_cast<float2*>(p.part_o + ((int64_t)slot * HB + h) * D + e) = make_float2(v[0] * inv, v[1] * inv);
+          } else {
+            if (e < p.d) row[e] = from_f<T>(v[0] * inv);
+            if (e + 1 < p.d) row[e + 1] = from_f<T>(v[1] * inv);
+          }
         }
       }
       fresh = true;
     }
     cur.advance(p, segs, step + 1 < steps);
   }
+  cp_wait<0>();
   write_status(p.status, status);
 }
 
@@ -862,11 +966,15 @@ cudaError_t launch_mma(const DecodeParams& p, int ctas, cudaStream_t stream) {
                            32 * kJoinWarps, 0, stream, p);
 }
 
-template <typename T, int D>
+template <typename T, int D, int HB>
 cudaError_t launch_simt(const DecodeParams& p, int ctas, cudaStream_t stream) {
-  const cudaError_t e = launch_overlapped(paged_decode_simt_kernel<T, D>, ctas, kThreads, 0, stream, p);
+  constexpr int bytes = (int)sizeof(SimtSmem<T, D>);
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_simt_kernel<T, D, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       bytes);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(paged_decode_join_kernel<T, D, 8>, dim3(ctas * kWarps / kJoinWarps, 8), 32 * kJoinWarps, 0,
+  e = launch_overlapped(paged_decode_simt_kernel<T, D, HB>, ctas, kThreads, bytes, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(paged_decode_join_kernel<T, D, HB>, dim3(ctas * kWarps / kJoinWarps, HB), 32 * kJoinWarps, 0,
                            stream, p);
 }
 
@@ -885,7 +993,9 @@ cudaError_t launch_type(const DecodeParams& p, bool mma, int ctas, cudaStream_t 
     if (mma) return decode_pad_d(p.d) == 64 ? launch_mma_heads<T, 64>(p, ctas, stream)
                                             : launch_mma_heads<T, 128>(p, ctas, stream);
   }
-  return decode_pad_d(p.d) == 64 ? launch_simt<T, 64>(p, ctas, stream) : launch_simt<T, 128>(p, ctas, stream);
+  if (decode_pad_d(p.d) == 64)
+    return p.group <= 4 ? launch_simt<T, 64, 4>(p, ctas, stream) : launch_simt<T, 64, 8>(p, ctas, stream);
+  return p.group <= 4 ? launch_simt<T, 128, 4>(p, ctas, stream) : launch_simt<T, 128, 8>(p, ctas, stream);
 }
 
 }  // namespace
