@@ -331,6 +331,9 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   ptx::pdl_release();
   uint32_t status = 0;
   const uint32_t ring = ptx::smem_u32(sm.ring[warp]);
+  if (p.d < D)  // the columns past d, which no copy of a whole chunk fills
+    for (int i = lane; i < (int)sizeof(sm.ring[0]) / 16; i += 32)
+      reinterpret_cast<uint4*>(sm.ring[warp])[i] = make_uint4(0u, 0u, 0u, 0u);
   Cursor<kKeys> cur;
   Line line;
   const int steps = locate<kKeys>(p, segs, cur, line, status);
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   constexpr int kRowsAtOnce = 32 / kVecs;  // rows of one warp-wide copy
   const int vec = lane % kVecs, row_in = lane / kVecs;
   const bool vec_real = vec * 8 < p.d;
-  const bool whole_pages = (p.page_size & 15) == 0 && p.d == D;
+  const bool whole_pages = (p.page_size & 15) == 0;
   auto issue = [&]() {
     if (issued < steps) {
       const uint32_t seen = __ballot_sync(0xffffffffu, key_seen) & kAll;
@@ -380,8 +383,10 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
 #pragma unroll
           for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
             const uint32_t at = dst + (mt * 16 + i * kRowsAtOnce) * kPitch;
-            cp_async16(at, ks);
-            cp_async16(at + kKeys * kPitch, vs);
+            if (vec_real) {
+              cp_async16(at, ks);
+              cp_async16(at + kKeys * kPitch, vs);
+            }
             ks += kRowsAtOnce * p.k_tok;
             vs += kRowsAtOnce * p.v_tok;
           }
@@ -407,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
     }
     cp_commit();  // an empty group when there is nothing left: the count stays one per step
   };
+  __syncwarp();
   look_up();
   for (int i = 0; i < kStages - 1; ++i) issue();
   write_record<kKeys>(p, line, cur, steps);
