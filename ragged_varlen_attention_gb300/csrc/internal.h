@@ -375,6 +375,8 @@ struct DecodeParams {
   int32_t batch, h_q, h_kv, d, group;
   int32_t page_size, num_pages, max_pages;
   FastDiv by_page;
+  int32_t workers;          // warps of the launch
+  int32_t few;              // at most 256 requests, and the line's chunks fit 31 bits
   int32_t aligned;          // cache rows are whole 16-byte pieces (SIMT kernel)
   float scale_log2;
   uint32_t* status;
@@ -391,7 +393,7 @@ constexpr int decode_seg_heads(int group, bool mma) {
   return !mma ? (group <= 4 ? 4 : 8) : group <= 8 ? 8 : group <= 16 ? 16 : 32;
 }
 constexpr int decode_pad_d(int d) { return d <= 64 ? 64 : 128; }
-cudaError_t launch_paged_decode(const DecodeParams& p, thd_dtype_t dtype, bool mma, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_decode(DecodeParams p, thd_dtype_t dtype, bool mma, int num_sms, cudaStream_t stream);
 
 }  // namespace thd
 
@@ -430,6 +432,7 @@ struct thd_attn_plan_s {
   thd_norm_rope_desc_t ndesc;
   thd_paged_tables_desc_t tdesc;
   thd_paged_decode_desc_t ddesc;
+  int32_t few_requests;     // see DecodeParams::few
   // optional attention-kernel timing (thd_attn_profile_enable)
   int32_t prof_slots;
   int32_t prof_count;

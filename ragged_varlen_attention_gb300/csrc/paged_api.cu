@@ -278,12 +278,14 @@ thd_status_t thd_paged_decode_plan(thd_attn_plan_t* out, const thd_paged_decode_
   const int group = d.h_q / d.h_kv;
   const int seg_heads = thd::decode_seg_heads(group, mma);
   const int64_t segs = (int64_t)d.h_kv * ((group + seg_heads - 1) / seg_heads);
-  const int64_t max_chunks = (int64_t)d.max_pages * d.page_size / thd::kDecodeMinChunk + 2;
+  const int64_t max_chunks = (int64_t)d.max_pages * d.page_size / thd::kDecodeMinChunk + 3;
   // the line's chunks: below 2^31 for each worker, and chunks x workers inside 64 bits
   if ((double)d.batch * (double)segs * (double)max_chunks >= (double)(int64_t(1) << 38)) return THD_ERR_UNSUPPORTED;
+  const bool few = d.batch <= 256 && d.batch * segs * max_chunks < kInt32End;
   auto* p = new_plan(kPlanPagedDecode, thd::kDecodeMaxCtas);
   if (!p) return THD_ERR_INVALID_ARG;
   p->ddesc = d;
+  p->few_requests = few;
   p->elem_bytes = eb;
   p->scale = scale;
   p->kernel = mma ? THD_KERNEL_MMA : THD_KERNEL_SIMT;
@@ -325,6 +327,7 @@ thd_status_t thd_paged_decode(thd_attn_plan_t plan, const void* q, const void* k
   dp.batch = d.batch; dp.h_q = d.h_q; dp.h_kv = d.h_kv; dp.d = d.d; dp.group = d.h_q / d.h_kv;
   dp.page_size = d.page_size; dp.num_pages = d.num_pages; dp.max_pages = d.max_pages;
   dp.by_page = thd::FastDiv(d.page_size);
+  dp.few = plan->few_requests;
   const int64_t eb = plan->elem_bytes;
   dp.aligned = aligned(k_cache, 16) && aligned(v_cache, 16) && d.d * eb % 16 == 0;
   for (int i = 1; i < 3; ++i)

@@ -121,10 +121,80 @@ struct Line {
   }
 };
 
-// The number of chunks in the warp's range, and the cursor at its beginning. Every thread
-// calls it.
+__device__ __forceinline__ Line line_of(int64_t total) {
+  Line line;
+  line.total = total;
+  line.workers = (int32_t)min64((int64_t)gridDim.x * kWarps, max64(total, 1));
+  line.each = quotient(total, line.workers);  // below 2^31 by the plan's bound
+  line.extra = (int32_t)(total - (int64_t)line.each * line.workers);
+  return line;
+}
+
+__device__ __forceinline__ int32_t inclusive_scan(int32_t v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, v, s);
+    if (lane >= s) v += o;
+  }
+  return v;
+}
+
+// The number of chunks in the warp's range, and the cursor at its beginning. All lanes call
+// it. Each warp finds its own range, without a barrier: up to 256 requests, 128 at a time in
+// flight; lane l keeps the sum of requests 32 l .. 32 l + 31. The chunks of the line fit 31
+// bits. (With more requests the block shares them: locate_many.) A quarter of a small call's
+// time was here with the block-wide search.
 template <int KC>
-__device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC>& cur, Line& line, uint32_t& status) {
+__device__ __forceinline__ int locate_few(const DecodeParams& p, int segs, Cursor<KC>& cur, Line& line,
+                                          uint32_t& status) {
+  const int lane = threadIdx.x & 31;
+  int32_t tile_sum = 0, total = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 128) {
+    int32_t mine[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int b = b0 + 32 * t + lane;
+      mine[t] = 0;
+      if (b < p.batch) {
+        const Span s = span_of<KC>(p, b);
+        if (s.bad) status |= THD_DEV_BAD_LENGTH;
+        mine[t] = s.chunks;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int32_t sum = __reduce_add_sync(0xffffffffu, mine[t]);
+      if (lane == b0 / 32 + t) tile_sum = sum;
+      total += sum;
+    }
+  }
+  line = line_of((int64_t)total * segs);
+  const int32_t worker = blockIdx.x * kWarps + threadIdx.x / 32;
+  if (worker >= line.workers || total == 0) return 0;
+  const int32_t begin = (int32_t)line.start(worker);
+  int32_t before = 0, b0 = 0;
+  if (p.batch > 32) {
+    const int32_t upto = inclusive_scan(tile_sum);
+    const int tile = __ffs(__ballot_sync(0xffffffffu, begin < upto * segs)) - 1;
+    before = __shfl_sync(0xffffffffu, upto - tile_sum, tile);
+    b0 = tile * 32;
+  }
+  const int32_t mine = b0 + lane < p.batch ? span_of<KC>(p, b0 + lane).chunks : 0;
+  const int32_t upto = before + inclusive_scan(mine);
+  const int at = __ffs(__ballot_sync(0xffffffffu, begin < upto * segs)) - 1;
+  cur.b = b0 + at;
+  cur.sp = span_of<KC>(p, cur.b);
+  const int32_t rel = begin - __shfl_sync(0xffffffffu, upto - mine, at) * segs;
+  cur.seg = (int)((uint32_t)rel / (uint32_t)cur.sp.chunks);
+  cur.chunk = rel - cur.seg * cur.sp.chunks;
+  return (int)(line.start(worker + 1) - line.start(worker));
+}
+
+// The same for any number of requests and chunks: the block's threads share the requests.
+template <int KC>
+__device__ __forceinline__ int locate_many(const DecodeParams& p, int segs, Cursor<KC>& cur, Line& line,
+                                           uint32_t& status) {
   __shared__ int64_t warp_sums[kWarps];
   __shared__ int32_t found_b[kWarps];
   __shared__ int64_t found_before[kWarps];
@@ -150,10 +220,7 @@ __device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC
     if (w < warp) upto += warp_sums[w];
     total += warp_sums[w];
   }
-  line.total = total * segs;
-  line.workers = (int32_t)min64((int64_t)gridDim.x * kWarps, max64(line.total, 1));
-  line.each = quotient(line.total, line.workers);  // below 2^31 by the plan's bound
-  line.extra = (int32_t)(line.total - (int64_t)line.each * line.workers);
+  line = line_of(total * segs);
   // the request that each of the block's workers begins in
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -180,6 +247,11 @@ __device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC
   cur.seg = quotient(rel, cur.sp.chunks);
   cur.chunk = (int)(rel - (int64_t)cur.seg * cur.sp.chunks);
   return (int)(line.start(worker + 1) - line.start(worker));
+}
+
+template <int KC>
+__device__ __forceinline__ int locate(const DecodeParams& p, int segs, Cursor<KC>& cur, Line& line, uint32_t& status) {
+  return p.few ? locate_few(p, segs, cur, line, status) : locate_many(p, segs, cur, line, status);
 }
 
 // The worker's record for the join kernel, from the cursor at the beginning of its range.
@@ -297,7 +369,7 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 // its sum is kept in float32.
 //
 // A stage is filled by cp.async, 16 bytes a lane, 2 (d = 128) or 4 rows at a time. Where a
-// page holds a multiple of 16 rows and the whole chunk is visible, its rows are a constant
+// page holds a multiple of 8 rows and the whole chunk is visible, 8 rows are a constant
 // stride apart and cost an addition each; otherwise each row's page comes from the lane that
 // looked it up. Rows sit 16 bytes apart from a multiple of 128, so that ldmatrix's eight rows
 // fall into different banks without a swizzle, and every address in the loop is a constant
@@ -364,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   constexpr int kRowsAtOnce = 32 / kVecs;  // rows of one warp-wide copy
   const int vec = lane % kVecs, row_in = lane / kVecs;
   const bool vec_real = vec * 8 < p.d;
-  const bool whole_pages = (p.page_size & 15) == 0;
+  const bool whole_pages = (p.page_size & 7) == 0;  // 8 rows from a multiple of 8 are in one page
   auto issue = [&]() {
     if (issued < steps) {
       const uint32_t seen = __ballot_sync(0xffffffffu, key_seen) & kAll;
@@ -375,14 +447,14 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
       const T* vh = static_cast<const T*>(p.v) + (int64_t)g * p.v_head + vec * 8;
       if (whole_pages && seen == kAll) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int64_t at_k = __shfl_sync(0xffffffffu, key_k, mt * 16);
-          const int64_t at_v = same ? at_k : __shfl_sync(0xffffffffu, key_v, mt * 16);
+        for (int r8 = 0; r8 < kKeys; r8 += 8) {
+          const int64_t at_k = __shfl_sync(0xffffffffu, key_k, r8);
+          const int64_t at_v = same ? at_k : __shfl_sync(0xffffffffu, key_v, r8);
           const T* ks = kh + at_k + row_in * p.k_tok;
           const T* vs = vh + at_v + row_in * p.v_tok;
 #pragma unroll
-          for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
-            const uint32_t at = dst + (mt * 16 + i * kRowsAtOnce) * kPitch;
+          for (int i = 0; i < 8 / kRowsAtOnce; ++i) {
+            const uint32_t at = dst + (r8 + i * kRowsAtOnce) * kPitch;
             if (vec_real) {
               cp_async16(at, ks);
               cp_async16(at + kKeys * kPitch, vs);
@@ -415,40 +487,48 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   __syncwarp();
   look_up();
   for (int i = 0; i < kStages - 1; ++i) issue();
-  write_record<kKeys>(p, line, cur, steps);
-  write_empty<T>(p);
 
   uint32_t qf[D / 16][NT][2];
   float acc[D / 16][NT][4];
   float top[NT][2], sum[NT][2];
   int head0 = 0, heads = 0, first = 0;
-  bool fresh = true;
+  // the query rows of the segment at `cur`; with 8 heads there are registers to load them
+  // ahead of the last segment's end
+  constexpr bool kAhead = NT == 1;
+  auto load_q = [&]() {
+    first = cur.chunk;
+    heads = segment_heads<kHeads>(p, cur.seg, head0);
+    const T* q = static_cast<const T*>(p.q) + (int64_t)cur.b * p.q_tok;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + lane / 4;
+      const T* row = q + (int64_t)(head0 + h) * p.q_head;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = kk * 16 + j * 8 + (lane % 4) * 2;
+          qf[kk][nt][j] = h < heads && e < p.d ? *reinterpret_cast<const uint32_t*>(row + e) : 0u;
+        }
+    }
+  };
+  auto clear = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      top[nt][0] = top[nt][1] = -INFINITY;
+      sum[nt][0] = sum[nt][1] = 0.f;
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[dt][nt][j] = 0.f;
+    }
+  };
+  if (steps > 0) load_q();
+  clear();
+  write_record<kKeys>(p, line, cur, steps);
+  write_empty<T>(p);
   uint32_t stage = 0;
   for (int step = 0; step < steps; ++step) {
-    if (fresh) {
-      fresh = false;
-      first = cur.chunk;
-      heads = segment_heads<kHeads>(p, cur.seg, head0);
-      const T* q = static_cast<const T*>(p.q) + (int64_t)cur.b * p.q_tok;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int h = nt * 8 + lane / 4;
-        const T* row = q + (int64_t)(head0 + h) * p.q_head;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int e = kk * 16 + j * 8 + (lane % 4) * 2;
-            qf[kk][nt][j] = h < heads && e < p.d ? *reinterpret_cast<const uint32_t*>(row + e) : 0u;
-          }
-        top[nt][0] = top[nt][1] = -INFINITY;
-        sum[nt][0] = sum[nt][1] = 0.f;
-#pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[dt][nt][j] = 0.f;
-      }
-    }
     cp_wait<kStages - 2>();
     __syncwarp();
     const uint32_t seen = sm.seen[warp][stage];
@@ -544,11 +624,15 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
     issue();
     stage = stage + 1 == kStages ? 0 : stage + 1;
 
-    if (cur.chunk + 1 == cur.sp.chunks || step + 1 == steps) {
-      const int slot = piece_slot(worker, first, cur.chunk, cur.sp.chunks);
+    const bool last = cur.chunk + 1 == cur.sp.chunks || step + 1 == steps;
+    const int slot = piece_slot(worker, first, cur.chunk, cur.sp.chunks);
+    const int b_done = cur.b, head0_done = head0, heads_done = heads;
+    cur.advance(p, segs, step + 1 < steps);
+    if (last) {
+      if (kAhead && step + 1 < steps) load_q();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (nt * 8 >= heads) break;
+        if (nt * 8 >= heads_done) break;
         float inv[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -562,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
           const float lse2 = dead ? -INFINITY : top[nt][j] + log2f(l);
           if (lane < 4) {
             if (slot >= 0) p.part_lse[(int64_t)slot * kHeads + h] = lse2;
-            else if (h < heads && p.stats)
-              p.stats[(int64_t)cur.b * p.stats_tok + (int64_t)(head0 + h) * p.stats_head] = lse2 * kLn2;
+            else if (h < heads_done && p.stats)
+              p.stats[(int64_t)b_done * p.stats_tok + (int64_t)(head0_done + h) * p.stats_head] = lse2 * kLn2;
           }
         }
         if (slot >= 0) {
@@ -575,20 +659,20 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
             for (int j = 0; j < 4; ++j) row[(j & 1) * D + dt * 16 + (j >> 1) * 8] = acc[dt][nt][j] * inv[j & 1];
         } else {
           const int h = nt * 8 + lane / 4;
-          T* row = static_cast<T*>(p.o) + (int64_t)cur.b * p.o_tok + (int64_t)(head0 + h) * p.o_head;
+          T* row = static_cast<T*>(p.o) + (int64_t)b_done * p.o_tok + (int64_t)(head0_done + h) * p.o_head;
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const uint32_t v = transpose8x8(pack2<T>(acc[dt][nt][2 * half] * inv[0], acc[dt][nt][2 * half + 1] * inv[1]));
               const int e = dt * 16 + half * 8 + (lane % 4) * 2;
-              if (h < heads && e < p.d) *reinterpret_cast<uint32_t*>(row + e) = v;
+              if (h < heads_done && e < p.d) *reinterpret_cast<uint32_t*>(row + e) = v;
             }
         }
       }
-      fresh = true;
+      if (!kAhead && step + 1 < steps) load_q();
+      clear();
     }
-    cur.advance(p, segs, step + 1 < steps);
   }
   write_status(p.status, status);
 }
@@ -842,11 +926,13 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_simt_
 }
 
 // ----------------------------------------------------------------- join kernel
-// Block (x, h) looks at the records of 8 workers, a warp each, and merges the pieces of the
-// segments that they own for one head. The piece that begins the segment is slot
-// 2 (w - 1) + 1, the others are slots 2w, 2 (w + 1), ... Up to 8 pieces are the warp's own
-// work, more are shared by the block's warps (every eighth piece) and merged in warp order:
-// a long request alone leaves hundreds, and a warp would read them one latency after another.
+// Block (x, h) looks at the records of 16 workers and merges the pieces of the segments that
+// they own for one head. The piece that begins the segment is slot 2 (w - 1) + 1, the others
+// are slots 2w, 2 (w + 1), ... Up to 8 pieces are one warp's work, more are shared by the
+// block's warps (every eighth piece) and merged in warp order: a long request alone leaves
+// hundreds, and a warp would read them one latency after another. Every warp reads the 16
+// records and knows its share, so that only shared segments meet a barrier.
+constexpr int kJoinWorkers = 16;
 constexpr int kJoinWarps = 8;
 
 // The running result of a warp: base-2 maximum and sum, and the lane's elements.
@@ -871,7 +957,7 @@ struct Merged {
   // pieces first, first + step, ... of worker w's segment
   template <int HEADS>
   __device__ __forceinline__ void read(const DecodeParams& p, int w, int h, int pieces, int first, int step) {
-    constexpr int kAtOnce = 4;
+    constexpr int kAtOnce = 8;
     for (int i0 = first; i0 < pieces; i0 += kAtOnce * step) {
       float lse[kAtOnce], x[kAtOnce][kPer];
 #pragma unroll
@@ -912,33 +998,33 @@ struct Merged {
 };
 
 template <typename T, int D, int HEADS>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_decode_join_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 4) paged_decode_join_kernel(DecodeParams p) {
   __shared__ float part_o[kJoinWarps][D];
   __shared__ float part_max[kJoinWarps], part_sum[kJoinWarps];
-  __shared__ DecodeRec shared_rec[kJoinWarps];
   ptx::pdl_wait();
   ptx::pdl_release();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, h = blockIdx.y;
-  const int w = blockIdx.x * kJoinWarps + warp;
-  const DecodeRec rec = p.recs[w];
-  const bool many = rec.pieces > kJoinWarps;
-  if (lane == 0) shared_rec[warp] = rec;
+  const int w0 = blockIdx.x * kJoinWorkers;
+  // lane i: the record of worker w0 + i, if it owns a segment that has this head
+  DecodeRec rec = {0, 0, 0, 0};
+  if (lane < kJoinWorkers && w0 + lane < p.workers) rec = p.recs[w0 + lane];
+  int head0 = 0;
+  if (rec.pieces > 0 && h >= segment_heads<HEADS>(p, rec.seg, head0)) rec.pieces = 0;
+  const uint32_t few = __ballot_sync(0xffffffffu, rec.pieces > 0 && rec.pieces <= kJoinWarps);
+  const uint32_t many = __ballot_sync(0xffffffffu, rec.pieces > kJoinWarps);
   Merged<D> m;
-  if (rec.pieces > 0 && !many) {
-    int head0;
-    if (h < segment_heads<HEADS>(p, rec.seg, head0)) {
-      m.clear();
-      m.template read<HEADS>(p, w, h, rec.pieces, 0, 1);
-      m.template write<T>(p, rec.b, head0 + h);
-    }
-  }
-  if (!__syncthreads_or(many)) return;
-  for (int o = 0; o < kJoinWarps; ++o) {
-    const DecodeRec r = shared_rec[o];
-    int head0;
-    if (r.pieces <= kJoinWarps || h >= segment_heads<HEADS>(p, r.seg, head0)) continue;
+  int turn = 0;
+  for (uint32_t todo = few; todo; todo &= todo - 1) {
+    const int i = __ffs(todo) - 1;
+    if (turn++ % kJoinWarps != warp) continue;
     m.clear();
-    m.template read<HEADS>(p, blockIdx.x * kJoinWarps + o, h, r.pieces, warp, kJoinWarps);
+    m.template read<HEADS>(p, w0 + i, h, __shfl_sync(0xffffffffu, rec.pieces, i), 0, 1);
+    m.template write<T>(p, __shfl_sync(0xffffffffu, rec.b, i), __shfl_sync(0xffffffffu, head0, i) + h);
+  }
+  for (uint32_t todo = many; todo; todo &= todo - 1) {
+    const int i = __ffs(todo) - 1;
+    m.clear();
+    m.template read<HEADS>(p, w0 + i, h, __shfl_sync(0xffffffffu, rec.pieces, i), warp, kJoinWarps);
     __syncthreads();  // the last segment's results have been read
 #pragma unroll
     for (int k = 0; k < m.kPer; ++k) part_o[warp][lane * m.kPer + k] = m.o[k];
@@ -950,13 +1036,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_decode_join_kernel(Deco
     if (warp != 0) continue;
     m.clear();
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
+    for (int o = 0; o < kJoinWarps; ++o) {
       float x[m.kPer];
 #pragma unroll
-      for (int k = 0; k < m.kPer; ++k) x[k] = part_o[i][lane * m.kPer + k];
-      m.add(part_max[i], part_sum[i], x);
+      for (int k = 0; k < m.kPer; ++k) x[k] = part_o[o][lane * m.kPer + k];
+      m.add(part_max[o], part_sum[o], x);
     }
-    m.template write<T>(p, r.b, head0 + h);
+    m.template write<T>(p, __shfl_sync(0xffffffffu, rec.b, i), __shfl_sync(0xffffffffu, head0, i) + h);
   }
 }
 
@@ -968,7 +1054,7 @@ cudaError_t launch_mma(const DecodeParams& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_overlapped(paged_decode_mma_kernel<T, D, NT>, ctas, kThreads, bytes, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(paged_decode_join_kernel<T, D, 8 * NT>, dim3(ctas * kWarps / kJoinWarps, 8 * NT),
+  return launch_overlapped(paged_decode_join_kernel<T, D, 8 * NT>, dim3((p.workers + kJoinWorkers - 1) / kJoinWorkers, 8 * NT),
                            32 * kJoinWarps, 0, stream, p);
 }
 
@@ -980,7 +1066,7 @@ cudaError_t launch_simt(const DecodeParams& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_overlapped(paged_decode_simt_kernel<T, D, HB>, ctas, kThreads, bytes, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(paged_decode_join_kernel<T, D, HB>, dim3(ctas * kWarps / kJoinWarps, HB), 32 * kJoinWarps, 0,
+  return launch_overlapped(paged_decode_join_kernel<T, D, HB>, dim3((p.workers + kJoinWorkers - 1) / kJoinWorkers, HB), 32 * kJoinWarps, 0,
                            stream, p);
 }
 
@@ -1006,9 +1092,10 @@ cudaError_t launch_type(const DecodeParams& p, bool mma, int ctas, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const DecodeParams& p, thd_dtype_t dtype, bool mma, int num_sms, cudaStream_t stream) {
+cudaError_t launch_paged_decode(DecodeParams p, thd_dtype_t dtype, bool mma, int num_sms, cudaStream_t stream) {
   const int sms = num_sms < kMaxSmsForSizing ? num_sms : kMaxSmsForSizing;
-  const int ctas = sms * kDecodeCtasPerSm;  // even: the join kernel takes 8 workers a block
+  const int ctas = sms * kDecodeCtasPerSm;
+  p.workers = ctas * kWarps;
   switch (dtype) {
     case THD_BF16: return launch_type<__nv_bfloat16>(p, mma, ctas, stream);
     case THD_FP16: return launch_type<__half>(p, mma, ctas, stream);

@@ -41,14 +41,15 @@ __device__ __forceinline__ int32_t pages_of(const PagedTablesParams& p, int32_t 
 
 struct Request {
   int32_t len, need;
-  bool bad;
+  bool bad, bad_cu;  // takes no part; its offsets are outside the rows or decrease
 };
-// The request's length and pages; cu entries are inside [0, cap_rows] and ordered.
 __device__ __forceinline__ Request request_of(const PagedTablesParams& p, int b) {
   Request r;
+  const int lo = p.cu_new[b], hi = p.cu_new[b + 1];
   r.len = p.seq_lens[b];
-  const int64_t after = (int64_t)r.len + (p.cu_new[b + 1] - p.cu_new[b]);
-  r.bad = r.len < 0 || after > (int64_t)p.max_pages * p.page_size;
+  r.bad_cu = lo < 0 || hi < lo || hi > p.cap_rows;
+  const int64_t after = (int64_t)r.len + (r.bad_cu ? 0 : hi - lo);
+  r.bad = r.bad_cu || r.len < 0 || after > (int64_t)p.max_pages * p.page_size;
   r.need = r.bad ? 0 : pages_of(p, (int32_t)after) - pages_of(p, r.len);
   return r;
 }
@@ -64,23 +65,25 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(PagedTablesParam
   const int strip = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.batch, (int)threadIdx.x * strip), b1 = min(p.batch, b0 + strip);
 
+  // the lengths, the offsets and the free list's span in one round of loads
+  int64_t begin = p.free_span[0], end = p.free_span[1];
   int bad_cu = 0;
+  int64_t need = 0;
   for (int b = b0; b < b1; ++b) {
-    const int lo = p.cu_new[b], hi = p.cu_new[b + 1];
-    if (lo < 0 || hi < lo || hi > p.cap_rows) bad_cu = 1;
+    const Request r = request_of(p, b);
+    bad_cu |= r.bad_cu;
+    need += r.need;
   }
   bad_cu = __syncthreads_or(bad_cu);
-  int64_t begin = p.free_span[0], end = p.free_span[1];
   if (begin < 0 || end < begin || end > p.cap_free) {
     status |= THD_DEV_BAD_OFFSET;
     end = begin;
   }
   const int64_t avail = end - begin;
-  if (bad_cu) status |= THD_DEV_BAD_LENGTH;
-
-  int64_t need = 0;
-  if (!bad_cu)
-    for (int b = b0; b < b1; ++b) need += request_of(p, b).need;
+  if (bad_cu) {
+    status |= THD_DEV_BAD_LENGTH;
+    need = 0;
+  }
   const int64_t upto = block_scan(need, warp_sums);
   int64_t at = upto - need;
   for (int b = b0; b < b1; ++b) {
