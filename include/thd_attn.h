@@ -548,7 +548,8 @@ typedef struct {
   int64_t bytes[4];               /* 0 = not checked */
   thd_stats_layout_t stats_layout;/* head-major: head stride `batch` */
   float softmax_scale;            /* NaN => 1/sqrt(d) */
-  thd_kernel_t kernel;            /* AUTO: MMA for bf16/fp16 with d % 8 == 0 and 16-byte cache strides, else SIMT */
+  thd_kernel_t kernel;            /* AUTO: MMA for bf16/fp16 with d % 8 == 0, cache strides
+                                     of whole 16 bytes below 2^31 and even Q and O strides, else SIMT */
   uint32_t flags;                 /* none defined; must be 0 */
 } thd_paged_decode_desc_t;
 

@@ -264,7 +264,9 @@ thd_status_t thd_paged_decode_plan(thd_attn_plan_t* out, const thd_paged_decode_
     if (d.stride_tok[i] < 0 || d.stride_head[i] < 0 || d.bytes[i] < 0 || (cache && d.stride_page[i] < 0))
       return THD_ERR_INVALID_ARG;
     if (cache)
-      mma = mma && d.stride_tok[i] * eb % 16 == 0 && d.stride_head[i] * eb % 16 == 0 && d.stride_page[i] * eb % 16 == 0;
+      mma = mma && d.stride_tok[i] * eb % 16 == 0 && d.stride_head[i] * eb % 16 == 0 &&
+            d.stride_page[i] * eb % 16 == 0 && d.stride_tok[i] < kInt32End && d.stride_head[i] < kInt32End &&
+            d.stride_page[i] < kInt32End;
     else
       mma = mma && d.stride_tok[i] % 2 == 0 && d.stride_head[i] % 2 == 0;  // Q and O are accessed in pairs
     if (d.bytes[i] == 0) continue;

@@ -417,7 +417,10 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   // up one step before it is used
   bool key_seen = false;
   int64_t key_k = 0, key_v = 0;  // its rows' offsets in the caches
-  const bool same = p.k_page == p.v_page && p.k_tok == p.v_tok;
+  // the plan gives this kernel strides below 2^31: a product is one 32 x 32 -> 64 instruction
+  const int k_page = (int)p.k_page, k_tok = (int)p.k_tok, k_head = (int)p.k_head;
+  const int v_page = (int)p.v_page, v_tok = (int)p.v_tok, v_head = (int)p.v_head;
+  const bool same = k_page == v_page && k_tok == v_tok;
   auto look_up = [&]() {
     key_seen = false;
     if (issued >= steps) return;
@@ -427,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
       const int page = p.block_table[(int64_t)load.b * p.table_stride + column];
       key_seen = page >= 0 && page < p.num_pages;
       if (!key_seen) status |= THD_DEV_BAD_PAGE;
-      key_k = page * p.k_page + row * p.k_tok;
-      key_v = same ? key_k : page * p.v_page + row * p.v_tok;
+      key_k = (int64_t)page * k_page + (int64_t)row * k_tok;
+      key_v = same ? key_k : (int64_t)page * v_page + (int64_t)row * v_tok;
     }
   };
   constexpr uint32_t kAll = kKeys == 16 ? 0xffffu : 0xffffffffu;
@@ -437,21 +440,25 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   const int vec = lane % kVecs, row_in = lane / kVecs;
   const bool vec_real = vec * 8 < p.d;
   const bool whole_pages = (p.page_size & 7) == 0;  // 8 rows from a multiple of 8 are in one page
+  const T* const k_lane = static_cast<const T*>(p.k) + vec * 8;
+  const T* const v_lane = static_cast<const T*>(p.v) + vec * 8;
+  const int64_t k_row = (int64_t)row_in * k_tok, v_row = (int64_t)row_in * v_tok;
+  const int64_t k_step = (int64_t)kRowsAtOnce * k_tok, v_step = (int64_t)kRowsAtOnce * v_tok;
   auto issue = [&]() {
     if (issued < steps) {
       const uint32_t seen = __ballot_sync(0xffffffffu, key_seen) & kAll;
       if (lane == 0) sm.seen[warp][load_stage] = seen;
       const uint32_t dst = ring + load_stage * Smem::kStageBytes + row_in * kPitch + vec * 16;
-      const int g = load.seg / per;
-      const T* kh = static_cast<const T*>(p.k) + (int64_t)g * p.k_head + vec * 8;
-      const T* vh = static_cast<const T*>(p.v) + (int64_t)g * p.v_head + vec * 8;
+      const int g = per == 1 ? load.seg : load.seg / per;
+      const T* kh = k_lane + (int64_t)g * k_head;
+      const T* vh = v_lane + (int64_t)g * v_head;
       if (whole_pages && seen == kAll) {
 #pragma unroll
         for (int r8 = 0; r8 < kKeys; r8 += 8) {
           const int64_t at_k = __shfl_sync(0xffffffffu, key_k, r8);
           const int64_t at_v = same ? at_k : __shfl_sync(0xffffffffu, key_v, r8);
-          const T* ks = kh + at_k + row_in * p.k_tok;
-          const T* vs = vh + at_v + row_in * p.v_tok;
+          const T* ks = kh + (at_k + k_row);
+          const T* vs = vh + (at_v + v_row);
 #pragma unroll
           for (int i = 0; i < 8 / kRowsAtOnce; ++i) {
             const uint32_t at = dst + (r8 + i * kRowsAtOnce) * kPitch;
@@ -459,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
               cp_async16(at, ks);
               cp_async16(at + kKeys * kPitch, vs);
             }
-            ks += kRowsAtOnce * p.k_tok;
-            vs += kRowsAtOnce * p.v_tok;
+            ks += k_step;
+            vs += v_step;
           }
         }
       } else {
@@ -569,9 +576,9 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const bool see = (seen >> (mt * 16 + half * 8 + lane / 4)) & 1;
               float& v = s[mt][nt][j + 2 * half];
-              v = see ? v * p.scale_log2 : -INFINITY;
+              v *= p.scale_log2;
+              if (seen != kAll && !((seen >> (mt * 16 + half * 8 + lane / 4)) & 1)) v = -INFINITY;
               m = fmaxf(m, v);
             }
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
@@ -954,22 +961,21 @@ struct Merged {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) o[k] = o[k] * f + g * x[k];
   }
-  // pieces first, first + step, ... of worker w's segment
-  template <int HEADS>
+  // pieces first, first + step, ... of worker w's segment, N at a time in flight
+  template <int HEADS, int N>
   __device__ __forceinline__ void read(const DecodeParams& p, int w, int h, int pieces, int first, int step) {
-    constexpr int kAtOnce = 8;
-    for (int i0 = first; i0 < pieces; i0 += kAtOnce * step) {
-      float lse[kAtOnce], x[kAtOnce][kPer];
+    for (int i0 = first; i0 < pieces; i0 += N * step) {
+      float lse[N], x[N][kPer];
 #pragma unroll
-      for (int a = 0; a < kAtOnce; ++a) {
+      for (int a = 0; a < N; ++a) {
         const int i = i0 + a * step;
         lse[a] = -INFINITY;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) x[a][k] = 0.f;
         if (i < pieces) {
-          const int64_t row = (int64_t)(i == 0 ? 2 * w - 1 : 2 * (w + i - 1)) * HEADS + h;
+          const int row = (i == 0 ? 2 * w - 1 : 2 * (w + i - 1)) * HEADS + h;
           lse[a] = p.part_lse[row];
-          const float* src = p.part_o + row * D + (threadIdx.x & 31) * kPer;
+          const float* src = p.part_o + (int64_t)row * D + (threadIdx.x & 31) * kPer;
           if constexpr (kPer == 4) {
             const float4 v = *reinterpret_cast<const float4*>(src);
             x[a][0] = v.x; x[a][1] = v.y; x[a][2] = v.z; x[a][3] = v.w;
@@ -980,7 +986,7 @@ struct Merged {
         }
       }
 #pragma unroll
-      for (int a = 0; a < kAtOnce; ++a) add(lse[a], 1.f, x[a]);
+      for (int a = 0; a < N; ++a) add(lse[a], 1.f, x[a]);
     }
   }
   template <typename T>
@@ -1018,13 +1024,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) paged_decode_join_kernel(D
     const int i = __ffs(todo) - 1;
     if (turn++ % kJoinWarps != warp) continue;
     m.clear();
-    m.template read<HEADS>(p, w0 + i, h, __shfl_sync(0xffffffffu, rec.pieces, i), 0, 1);
+    m.template read<HEADS, 4>(p, w0 + i, h, __shfl_sync(0xffffffffu, rec.pieces, i), 0, 1);
     m.template write<T>(p, __shfl_sync(0xffffffffu, rec.b, i), __shfl_sync(0xffffffffu, head0, i) + h);
   }
   for (uint32_t todo = many; todo; todo &= todo - 1) {
     const int i = __ffs(todo) - 1;
     m.clear();
-    m.template read<HEADS>(p, w0 + i, h, __shfl_sync(0xffffffffu, rec.pieces, i), warp, kJoinWarps);
+    m.template read<HEADS, 8>(p, w0 + i, h, __shfl_sync(0xffffffffu, rec.pieces, i), warp, kJoinWarps);
     __syncthreads();  // the last segment's results have been read
 #pragma unroll
     for (int k = 0; k < m.kPer; ++k) part_o[warp][lane * m.kPer + k] = m.o[k];
