@@ -418,7 +418,7 @@ thd_status_t thd_indexer_topk(thd_attn_plan_t plan, const void* q_i, const void*
  *   thd_qk_norm_rope_paged   0 Q   1 K   2 V      3 Q out   4 K cache  5 V cache
  * Views marked -- are ignored. The outputs of fwd (and Q out of paged) may be the
  * inputs themselves (same pointer and strides), as dQ and dK may be dQ out and dK out;
- * any other overlap races.
+ * any other overlap races. Calls that overlap on the GPU need a workspace each.
  */
 typedef enum { THD_NORM_ROPE_FWD = 0, THD_NORM_ROPE_BWD = 1, THD_NORM_ROPE_PAGED = 2 } thd_norm_rope_form_t;
 
@@ -492,6 +492,7 @@ thd_status_t thd_qk_norm_rope_paged(thd_attn_plan_t plan, const void* q, const v
  * belong to no request are -1. No other entry of block_table is written.
  * The inputs seq_lens and free_span are not written, so that a call may be repeated;
  * a serving loop keeps two of each and swaps them. They must not be the outputs.
+ * Calls that overlap on the GPU need a workspace each.
  */
 typedef struct {
   int32_t batch;                  /* 0 .. 8192 */

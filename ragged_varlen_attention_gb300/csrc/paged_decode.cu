@@ -301,7 +301,7 @@ __device__ __forceinline__ int piece_slot(int worker, int first, int last, int c
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// 16 bytes of zeros when not `real` (src is not read then)
+// 16 bytes of zeros when not `real`: src is not read then, and is any valid aligned address
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
   const int bytes = real ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
           const int64_t at_v = same ? at_k : __shfl_sync(0xffffffffu, key_v, row);
           const bool real = ((seen >> row) & 1) && vec_real;
           const uint32_t at = dst + i * kRowsAtOnce * kPitch;
-          const T* ks = real ? kh + at_k : static_cast<const T*>(p.k);
-          const T* vs = real ? vh + at_v : static_cast<const T*>(p.v);
+          const void* ks = real ? static_cast<const void*>(kh + at_k) : p.status;
+          const void* vs = real ? static_cast<const void*>(vh + at_v) : p.status;
           cp_async16(at, ks, real);
           cp_async16(at + kKeys * kPitch, vs, real);
         }
@@ -767,8 +767,8 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_simt_
           const int row = i * kRowsAtOnce + row_in;
           const int64_t at_k = __shfl_sync(0xffffffffu, key_k, row), at_v = __shfl_sync(0xffffffffu, key_v, row);
           const bool real = ((seen >> row) & 1) && vec < p.d;
-          cp_async16(ptx::smem_u32(&rows[row][vec]), real ? kh + at_k + vec : static_cast<const T*>(p.k), real);
-          cp_async16(ptx::smem_u32(&rows[kKeys + row][vec]), real ? vh + at_v + vec : static_cast<const T*>(p.v), real);
+          cp_async16(ptx::smem_u32(&rows[row][vec]), real ? static_cast<const void*>(kh + at_k + vec) : p.status, real);
+          cp_async16(ptx::smem_u32(&rows[kKeys + row][vec]), real ? static_cast<const void*>(vh + at_v + vec) : p.status, real);
         }
       } else {
         for (int row = 0; row < kKeys; ++row) {

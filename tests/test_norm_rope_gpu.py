@@ -239,6 +239,41 @@ def test_in_place():
     assert torch.equal(q, out[0]) and torch.equal(k, out[1])
 
 
+@pytest.mark.parametrize("d,rot", [(128, 128), (57, 12)])
+def test_backward_in_place(d, rot):
+    q, k, _, w_q, w_k, table, pos = make(18, 333, 8, 2, d, rot, torch.float32)
+    dz = [torch.randn(t.shape, device="cuda") for t in (q, k)]
+    keep = [t.clone() for t in dz]
+    ref = rva.thd_qk_norm_rope_backward(q, k, *keep, w_q, w_k, table, pos, dq=dz[0].clone(), dk=dz[1].clone())
+    got = rva.thd_qk_norm_rope_backward(q, k, *dz, w_q, w_k, table, pos, dq=dz[0], dk=dz[1])
+    assert got[0] is dz[0] and all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("h_q,h_kv,d", [(8, 8, 128), (16, 4, 128), (6, 3, 64), (16, 16, 64), (5, 5, 256)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_units_that_span_tokens_and_units_of_one(h_q, h_kv, d, dtype):
+    """More rows than the grid takes at once, for each division of heads into units: every row is
+    the row that a call on it alone gives."""
+    rows = 5003
+    q, k, _, w_q, w_k, table, pos = make(rows, rows, h_q, h_kv, d, d, dtype)
+    out = rva.thd_qk_norm_rope_forward(q, k, w_q, w_k, table, pos)
+    dz = [torch.randn(t.shape, device="cuda").to(dtype) for t in (q, k)]
+    grads = rva.thd_qk_norm_rope_backward(q, k, dz[0], dz[1], w_q, w_k, table, pos)
+    some = torch.tensor([0, 1, 777, rows // 2, 2501, rows - 2, rows - 1], device="cuda")
+    a = rva.thd_qk_norm_rope_forward(q[some], k[some], w_q, w_k, table, pos[some])
+    b = rva.thd_qk_norm_rope_backward(q[some], k[some], dz[0][some], dz[1][some], w_q, w_k, table, pos[some])
+    for whole, part in zip(out + grads[:2], a + b[:2]):
+        assert torch.equal(whole[some], part)
+    # dw over everything: sums of 5003 x heads terms of at most u(32) each, over fewer than 256 levels
+    for x, z, w, dw in ((q, dz[0], w_q, grads[2]), (k, dz[1], w_k, grads[3])):
+        live = (pos >= 0).cpu().numpy()
+        xs, zs = f64(x), f64(z)
+        _, ref = norm_rope_bwd(xs, zs, f64(w), f64(table), pos.cpu().numpy(), 1e-6, False, np.zeros(x.shape))
+        xh = np.abs(xs) / np.sqrt((xs * xs).mean(-1, keepdims=True) + 1e-6)
+        bound = 288 * U * (pair_sum(zs, d, False) * xh)[live].sum((0, 1))
+        assert (np.abs(f64(dw) - ref) <= bound).all()
+
+
 def test_vector_and_any_size_kernels_agree():
     """The same values through views that allow wide accesses and through views that do not."""
     q, k, _, w_q, w_k, table, pos = make(19, 40, 6, 2, 64, 32, torch.bfloat16)
@@ -338,6 +373,18 @@ def test_on_a_given_stream():
         got = rva.thd_qk_norm_rope_forward(q, k, w_q, w_k, table, pos, stream=s)
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_on_the_current_stream():
+    q, k, _, w_q, w_k, table, pos = make(42, 300, 8, 2, 128, 128, torch.bfloat16)
+    ref = rva.thd_qk_norm_rope_forward(q, k, w_q, w_k, table, pos)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        late = q.clone().mul_(1)     # made on the side stream: the call has to come after it
+        got = rva.thd_qk_norm_rope_forward(late, k, w_q, w_k, table, pos)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
 def test_no_rows():

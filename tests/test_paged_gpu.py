@@ -242,6 +242,66 @@ def test_windows(window, dtype):
     check(cache, q, o, stats.view(4, 8), window=win, matrix=dtype != torch.float32)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("batch", [31, 32, 33, 127, 129, 255, 256, 257])
+def test_request_counts_around_the_search_steps(batch, dtype):
+    """The first worker of every request is found by 32, 128 and 256 requests at a time."""
+    lens = np.random.default_rng(batch).integers(0, 40, batch)
+    lens[batch // 2:batch // 2 + 20] = 0
+    cache = Cache(batch, lens.tolist(), 1, 64, 8, dtype, cols=6)
+    q = random_q(cache, 2)
+    o, stats = rva.thd_paged_attention(q, cache.k, cache.v, cache.table, cache.lens)
+    check(cache, q, o, stats.view(batch, 2), matrix=dtype != torch.float32)
+
+
+def test_views_of_other_layouts():
+    """Caches inside larger buffers, K and V of different strides, and an O whose odd strides
+    only the SIMT kernel takes."""
+    lens = [130, 47, 300]
+    cache = Cache(21, lens, 2, 128, 16, torch.bfloat16)
+    q = random_q(cache, 8)
+    ref = rva.thd_paged_attention(q, cache.k, cache.v, cache.table, cache.lens)
+    both = torch.full((cache.pages, 3, 16, 2, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+    k, v = both[:, 1, :, :, 128:], torch.full((cache.pages, 2, 16, 128), float("nan"), dtype=torch.bfloat16,
+                                              device="cuda").transpose(1, 2)
+    k.copy_(cache.k)
+    v.copy_(cache.v)
+    got = rva.thd_paged_attention(q, k, v, cache.table, cache.lens)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    for gap in (1, 129):
+        o = torch.zeros((3, 8, 128 + gap), dtype=torch.bfloat16, device="cuda")[..., :128]
+        rva.thd_paged_attention(q, cache.k, cache.v, cache.table, cache.lens, o=o, stats=ref[1])
+        check(cache, q, o, ref[1].view(3, 8), matrix=False)
+
+
+def test_odd_page_sizes_and_partly_visible_chunks():
+    """Every page size at which rows of a chunk lie in one page, in several, or in pages of their
+    own, with windows that begin and end inside a chunk."""
+    for page in (1, 2, 3, 8, 12, 24, 40, 257):
+        for dtype, d in ((torch.float16, 64), (torch.bfloat16, 128), (torch.bfloat16, 88), (torch.float32, 100)):
+            cache = Cache(page + d, [200, 77, 129, 8], 2, d, page, dtype)
+            q = random_q(cache, 6)
+            win = ints([-1, 50, 100, 3])
+            o, stats = rva.thd_paged_attention(q, cache.k, cache.v, cache.table, cache.lens, window_left=win)
+            check(cache, q, o, stats.view(4, 6), window=win, matrix=dtype != torch.float32)
+
+
+def test_an_empty_cache_and_no_requests():
+    """No page at all: every key is in a bad page. No request: nothing happens, status 0."""
+    for dtype in (torch.bfloat16, torch.float32):
+        k = torch.zeros((0, 16, 2, 64), dtype=dtype, device="cuda")
+        q = torch.ones((2, 4, 64), dtype=dtype, device="cuda")
+        table, lens = ints([[0, 1], [5, -1]]), ints([20, 3])
+        o, stats = torch.full_like(q, 7), torch.zeros(8, device="cuda")
+        plan = rva.paged_decode_plan_for_tensors(q, k, k, o, table)
+        ws = rva.alloc_workspace(plan, "cuda")
+        rva.thd_paged_decode(plan, q, k, k, table, lens, None, o, stats, ws)
+        assert rva.thd_attn_read_status(plan, ws) == bd.DEV_BAD_PAGE
+        assert (o == 0).all() and (stats == float("-inf")).all()
+        none = rva.thd_paged_attention(q[:0], k, k, table[:0], lens[:0])
+        assert none[0].shape == (0, 4, 64)
+
+
 def test_many_requests_most_of_them_empty():
     rng = np.random.default_rng(8)
     lens = np.where(rng.random(700) < 0.8, 0, rng.integers(1, 90, 700))
