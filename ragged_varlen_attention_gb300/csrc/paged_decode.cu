@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   uint32_t stage = 0;
   for (int step = 0; step < steps; ++step) {
     cp_wait<kStages - 2>();
-    __syncwarp();
+    __syncwarp();  // this stage has arrived for every lane, and every lane has read the last one
+    issue();       // which is filled again
     const uint32_t seen = sm.seen[warp][stage];
     const uint32_t kbase = ring + stage * Smem::kStageBytes;
     const uint32_t vbase = kbase + kKeys * kPitch;
@@ -564,14 +565,16 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[mt][nt][j] += odd[nt][j];
       }
-      uint32_t pb[MT][NT][2];
-      float scale[NT][2];
-      bool moved = false;
+      // The reference of the exponentials moves only when a score passes it by 2^8: weights up
+      // to 256 cost no precision (P is rounded relative to itself), and most chunks need neither
+      // the maximum over the lanes nor the rescaling.
+      bool over = false;
+      float m[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float m = -INFINITY;
+          m[nt][j] = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -579,40 +582,50 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
               float& v = s[mt][nt][j + 2 * half];
               v *= p.scale_log2;
               if (seen != kAll && !((seen >> (mt * 16 + half * 8 + lane / 4)) & 1)) v = -INFINITY;
-              m = fmaxf(m, v);
+              m[nt][j] = fmaxf(m[nt][j], v);
             }
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          m = fmaxf(m, top[nt][j]);
-          const float ref = m == -INFINITY ? 0.f : m;
-          scale[nt][j] = ptx::ex2(top[nt][j] - ref);
-          moved |= m != top[nt][j];
-          top[nt][j] = m;
-          float add = 0.f;
+          over |= m[nt][j] > top[nt][j] + 8.f;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float now = m[nt][j];
+            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 4));
+            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
+            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
+            now = fmaxf(now, top[nt][j]);
+            const float scale = ptx::ex2(top[nt][j] - (now == -INFINITY ? 0.f : now));
+            top[nt][j] = now;
+            sum[nt][j] *= scale;
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              acc[dt][nt][j] *= scale;
+              acc[dt][nt][j + 2] *= scale;
+            }
+          }
+      }
+      uint32_t pb[MT][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float ref = top[nt][j] == -INFINITY ? 0.f : top[nt][j];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               float& v = s[mt][nt][j + 2 * half];
               v = ptx::ex2(v - ref);
-              add += v;
+              sum[nt][j] += v;
             }
-          sum[nt][j] = sum[nt][j] * scale[nt][j] + add;
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           pb[mt][nt][0] = transpose8x8(pack2<T>(s[mt][nt][0], s[mt][nt][1]));
           pb[mt][nt][1] = transpose8x8(pack2<T>(s[mt][nt][2], s[mt][nt][3]));
         }
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[dt][nt][j] *= scale[nt][j & 1];
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -627,8 +640,6 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
         }
       }
     }
-    __syncwarp();  // the stage is read by every lane before it is filled again
-    issue();
     stage = stage + 1 == kStages ? 0 : stage + 1;
 
     const bool last = cur.chunk + 1 == cur.sp.chunks || step + 1 == steps;
@@ -822,6 +833,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_simt_
     }
     cp_wait<kStages - 2>();
     __syncwarp();
+    issue();
     const uint32_t seen = sm.seen[warp][stage];
     const T(*rows)[D] = sm.ring[warp][stage];
 #pragma unroll
@@ -889,8 +901,6 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_simt_
         }
       }
     }
-    __syncwarp();  // the stage is read by every lane before it is filled again
-    issue();
     stage = stage + 1 == kStages ? 0 : stage + 1;
 
     if (cur.chunk + 1 == cur.sp.chunks || step + 1 == steps) {
