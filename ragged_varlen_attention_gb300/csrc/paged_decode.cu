@@ -371,17 +371,19 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 // A stage is filled by cp.async, 16 bytes a lane, 2 (d = 128) or 4 rows at a time. Where a
 // page holds a multiple of 8 rows and the whole chunk is visible, 8 rows are a constant
 // stride apart and cost an addition each; otherwise each row's page comes from the lane that
-// looked it up. Rows sit 16 bytes apart from a multiple of 128, so that ldmatrix's eight rows
-// fall into different banks without a swizzle, and every address in the loop is a constant
-// away from the stage's. (One bulk copy per row instead, by the lane that knows the page, was
-// slower: the copy unit takes 11 to 15 cycles a row, 3.4 TB/s at d = 64, 4.95 at d = 128.)
+// looked it up. The 16-byte piece c of row r lies at c ^ (r & 7), so that ldmatrix's eight rows
+// fall into different banks. (Rows 16 bytes apart from a multiple of 128 do that too, with
+// addresses that are constants away from the stage's, but then half of the 32-byte sectors end
+// in two lines of shared memory and are requested twice: 38 % hits in L2 where nothing is read
+// again. One bulk copy per row, by the lane that knows the page, takes the copy unit 11 to 15
+// cycles: 3.4 TB/s at d = 64, 4.95 at d = 128.)
 template <int D>
 struct MmaSmem {
   static constexpr int kKeys = chunk_keys(D);
   static constexpr int kStages = 3;
-  static constexpr int kPitch = 2 * D + 16;
+  static constexpr int kPitch = 2 * D;
   static constexpr int kStageBytes = 2 * kKeys * kPitch;  // K rows, then V rows
-  unsigned char ring[kWarps][kStages][kStageBytes];
+  alignas(256) unsigned char ring[kWarps][kStages][kStageBytes];
   uint32_t seen[kWarps][kStages];  // bit r: key r of the stage is visible
 };
 
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   constexpr int MT = kKeys / 16;          // 16-key rows of the instruction in a chunk
   constexpr int kHeads = 8 * NT;
   constexpr int kPitch = Smem::kPitch;
-  extern __shared__ __align__(128) unsigned char raw[];
+  extern __shared__ __align__(1024) unsigned char raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int worker = blockIdx.x * kWarps + warp;
@@ -440,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
   const int vec = lane % kVecs, row_in = lane / kVecs;
   const bool vec_real = vec * 8 < p.d;
   const bool whole_pages = (p.page_size & 7) == 0;  // 8 rows from a multiple of 8 are in one page
+  const uint32_t piece = (vec ^ row_in) * 16;  // of row row_in (below 8); rows i kRowsAtOnce on: ^ their number
   const T* const k_lane = static_cast<const T*>(p.k) + vec * 8;
   const T* const v_lane = static_cast<const T*>(p.v) + vec * 8;
   const int64_t k_row = (int64_t)row_in * k_tok, v_row = (int64_t)row_in * v_tok;
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
     if (issued < steps) {
       const uint32_t seen = __ballot_sync(0xffffffffu, key_seen) & kAll;
       if (lane == 0) sm.seen[warp][load_stage] = seen;
-      const uint32_t dst = ring + load_stage * Smem::kStageBytes + row_in * kPitch + vec * 16;
+      const uint32_t dst = ring + load_stage * Smem::kStageBytes + row_in * kPitch;
       const int g = per == 1 ? load.seg : load.seg / per;
       const T* kh = k_lane + (int64_t)g * k_head;
       const T* vh = v_lane + (int64_t)g * v_head;
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
           const T* vs = vh + (at_v + v_row);
 #pragma unroll
           for (int i = 0; i < 8 / kRowsAtOnce; ++i) {
-            const uint32_t at = dst + (r8 + i * kRowsAtOnce) * kPitch;
+            const uint32_t at = dst + (r8 + i * kRowsAtOnce) * kPitch + (piece ^ (i * kRowsAtOnce * 16));
             if (vec_real) {
               cp_async16(at, ks);
               cp_async16(at + kKeys * kPitch, vs);
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
           const int64_t at_k = __shfl_sync(0xffffffffu, key_k, row);
           const int64_t at_v = same ? at_k : __shfl_sync(0xffffffffu, key_v, row);
           const bool real = ((seen >> row) & 1) && vec_real;
-          const uint32_t at = dst + i * kRowsAtOnce * kPitch;
+          const uint32_t at = dst + i * kRowsAtOnce * kPitch + (piece ^ ((i * kRowsAtOnce & 7) * 16));
           const void* ks = real ? static_cast<const void*>(kh + at_k) : p.status;
           const void* vs = real ? static_cast<const void*>(vh + at_v) : p.status;
           cp_async16(at, ks, real);
@@ -552,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[mt][nt][j] = odd[nt][j] = 0.f;
         // matrices in order: keys 0-7 / d 0-7, keys 8-15 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 8-15
-        const uint32_t at = kbase + (mt * 16 + (lane & 15)) * kPitch + (lane >> 4) * 16;
+        const uint32_t at = kbase + (mt * 16 + (lane & 15)) * kPitch + (((lane >> 4) ^ (lane & 7)) * 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           uint32_t a[4];
-          ldsm4(a, at + kk * 32);
+          ldsm4(a, at ^ (kk * 32));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816<T>(kk & 1 ? odd[nt] : s[mt][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
         }
@@ -630,11 +633,12 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         // matrices in order: keys 0-7 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 0-7, keys 8-15 / d 8-15
-        const uint32_t at = vbase + (mt * 16 + (lane & 7) + ((lane >> 4) << 3)) * kPitch + ((lane >> 3) & 1) * 16;
+        const uint32_t at =
+            vbase + (mt * 16 + (lane & 7) + ((lane >> 4) << 3)) * kPitch + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) {
           uint32_t a[4];
-          ldsm4_t(a, at + dt * 32);
+          ldsm4_t(a, at ^ (dt * 32));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816<T>(acc[dt][nt], a, pb[mt][nt][0], pb[mt][nt][1]);
         }
@@ -732,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_simt_
   constexpr int kKeys = Smem::kKeys, kStages = Smem::kStages;
   constexpr int kPer = D / 32, kPairs = kPer / 2;
   constexpr int NK = 32 / HB;
-  extern __shared__ __align__(128) unsigned char raw[];
+  extern __shared__ __align__(1024) unsigned char raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int worker = blockIdx.x * kWarps + warp;
