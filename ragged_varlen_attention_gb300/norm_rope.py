@@ -244,5 +244,9 @@ class ThdQkNormRope(torch.autograd.Function):
 def thd_qk_norm_rope(q, k, w_q, w_k, cos_sin, positions, *, eps: float = 1e-6, interleaved: bool = False):
     """Differentiable per-head norm and rotation of Q [rows, h_q, d] and K [rows, h_kv, d]
     (see ``thd_qk_norm_rope_fwd`` in include/thd_attn.h), as :func:`thd_attention` reads
-    them. Gradients flow to q, k, w_q and w_k; rows of negative position give zeros."""
+    them. Gradients flow to q, k, w_q and w_k; rows of negative position give zeros.
+
+    Forward and backward may be captured into one CUDA graph. As for any backward pass that
+    torch captures, drop the eager graphs over the same leaves first: torch accumulates into a
+    leaf on the stream that its living graph was made on, which a capture does not allow."""
     return ThdQkNormRope.apply(q, k, w_q, w_k, cos_sin, positions, float(eps), bool(interleaved))

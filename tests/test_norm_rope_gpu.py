@@ -364,6 +364,36 @@ def test_equal_inputs_give_equal_bits_and_graph_replays_see_new_inputs():
     assert all(torch.equal(s, t) for s, t in zip(out + grads, ref + ref_g))
 
 
+def test_a_captured_training_step_replays():
+    """Forward and backward through autograd and packed attention in one CUDA graph, after a
+    warm-up on a side stream whose eager graph is gone; against the same step made eagerly."""
+    h_q, h_kv, d = 4, 2, 64
+    x, y, v, w, _, table, _ = make(47, 90, h_q, h_kv, d, d, torch.bfloat16, pad=False)
+    pos = torch.arange(90, device="cuda").int() % 45
+    cu, mask = torch.tensor([0, 45, 90], dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int8, device="cuda")
+    leaves = [t.detach().clone().requires_grad_(True) for t in (x, y, v, w)]
+
+    def step():
+        qz, kz = rva.thd_qk_norm_rope(leaves[0], leaves[1], leaves[3], leaves[3], table, pos)
+        o = rva.thd_attention(qz, kz, leaves[2], cu, cu, mask_type=mask)
+        return torch.autograd.grad(o.float().square().sum(), leaves)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    with torch.no_grad():
+        leaves[0].mul_(-0.5)
+        leaves[3].add_(0.25)
+    graph.replay()
+    ref = step()
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
 def test_on_a_given_stream():
     q, k, _, w_q, w_k, table, pos = make(41, 300, 8, 2, 128, 128, torch.bfloat16)
     ref = rva.thd_qk_norm_rope_forward(q, k, w_q, w_k, table, pos)
