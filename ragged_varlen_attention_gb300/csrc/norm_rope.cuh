@@ -13,6 +13,12 @@
 // ones the backward was bound by them, 41 % of the copy bandwidth). A warp's unit is kUnroll x
 // (32/G) consecutive rows of one tensor, and the next unit's rows are loaded before
 // this one's are computed, so that loads are always in flight.
+//
+// Measured, bf16, 32 + 8 heads of d = 128, against a copy at 6.79 TB/s: forward 32768 tokens
+// 106 us (94 %), backward 16384 tokens 83 us (90 %), serving form 8192 tokens of 40 + 8 + 8
+// fp16 heads 40 us (88 %); 48 tokens of a decode step 2.6 us, where the launch and two memory
+// latencies are all there is. Where a unit spans tokens (heads that its rows do not divide)
+// each row has a table row of its own: 23889 tokens of 16 + 4 heads 46 us (79 %).
 #pragma once
 
 #include <cuda_bf16.h>

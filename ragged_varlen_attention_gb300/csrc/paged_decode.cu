@@ -15,6 +15,15 @@
 //   - A segment that lies inside one warp's range is finished there. One that crosses a
 //     border leaves normalised partial outputs in the workspace, and the join kernel
 //     merges them in the line's order (no atomics: equal inputs give equal bits).
+//
+// Measured (both kernels), against a copy at 6.79 TB/s: bf16, 64 requests of 1 to 8192 keys, 32 + 8
+// heads of d = 128 (1.07 GB) 172 us (92 %); fp16, 2 x 131072 keys, 64 + 8 heads 167 us (95 %);
+// 1024 x 256 keys 186 us (85 %: a segment's beginning and end cost about a chunk's time each);
+// d = 64, one query head per kv head, pages of 24, a window of 1023 keys (142 MB) 35 us (60 %);
+// float32, 32 + 8 heads 176 us (90 %), 64 + 8 heads 245 us (65 %: bound by the fma and shuffles);
+// 16 heads a group, pages of one row 64 us for 254 MB (58 %). One request of 700 keys takes 7.8 us:
+// 2.5 us until each warp knows its range and 1.4 until its keys are there, 2 to compute, the rest in
+// the join kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -361,12 +370,49 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// the larger magnitudes of two pairs (a NaN gives the other), and whether one is infinite
+template <typename T>
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t max_magnitude<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 v = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), __habs2(*reinterpret_cast<__nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t max_magnitude<__half>(uint32_t a, uint32_t b) {
+  const __half2 v = __hmax2(*reinterpret_cast<__half2*>(&a), __habs2(*reinterpret_cast<__half2*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ bool is_infinite(uint32_t magnitudes);
+template <>
+__device__ __forceinline__ bool is_infinite<__nv_bfloat16>(uint32_t m) {
+  return (m & 0xffffu) == 0x7f80u || (m >> 16) == 0x7f80u;
+}
+template <>
+__device__ __forceinline__ bool is_infinite<__half>(uint32_t m) {
+  return (m & 0xffffu) == 0x7c00u || (m >> 16) == 0x7c00u;
+}
+
 // ------------------------------------------------- matrix-instruction kernel
 // 16 keys are the rows of the instruction and the query heads its 8 columns: S^T = K Q^T,
 // then O^T += V^T P^T, so a group of 8 heads fills the tile (the other way round heads
-// would be padded to 16). P^T's fragment is S^T's, transposed 8 x 8 by movmatrix; P is
-// rounded to the storage type for the product (at most half a step of a value <= 1),
-// its sum is kept in float32.
+// would be padded to 16). P^T's fragment is S^T's, transposed 8 x 8 by movmatrix. P goes into
+// the product as two 16-bit parts, its rounding and what that left over: rounded once, its
+// error would be as large as O's own rounding (1.35 to 1.45 times the error in all, measured
+// against 64 bits). The second part is left out where a V is infinite, which a negative or
+// zero remainder would turn into NaN. Its sum is kept in float32.
 //
 // A stage is filled by cp.async, 16 bytes a lane, 2 (d = 128) or 4 rows at a time. Where a
 // page holds a multiple of 8 rows and the whole chunk is visible, 8 rows are a constant
@@ -609,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
             }
           }
       }
-      uint32_t pb[MT][NT][2];
+      uint32_t pb[MT][NT][2], rest[MT][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -625,23 +671,41 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm) paged_decode_mma_k
             }
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          pb[mt][nt][0] = transpose8x8(pack2<T>(s[mt][nt][0], s[mt][nt][1]));
-          pb[mt][nt][1] = transpose8x8(pack2<T>(s[mt][nt][2], s[mt][nt][3]));
-        }
-      }
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        // matrices in order: keys 0-7 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 0-7, keys 8-15 / d 8-15
-        const uint32_t at =
-            vbase + (mt * 16 + (lane & 7) + ((lane >> 4) << 3)) * kPitch + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
+          for (int half = 0; half < 2; ++half) {
+            const float x = s[mt][nt][2 * half], y = s[mt][nt][2 * half + 1];
+            const uint32_t rounded = pack2<T>(x, y);
+            const float2 back = unpack2<T>(rounded);
+            pb[mt][nt][half] = transpose8x8(rounded);
+            rest[mt][nt][half] = transpose8x8(pack2<T>(x - back.x, y - back.y));
+          }
+      }
+      // matrices in order: keys 0-7 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 0-7, keys 8-15 / d 8-15
+      const uint32_t v_at =
+          vbase + ((lane & 7) + ((lane >> 4) << 3)) * kPitch + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
+      uint32_t largest = 0;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) {
           uint32_t a[4];
-          ldsm4_t(a, at ^ (dt * 32));
+          ldsm4_t(a, (v_at + mt * 16 * kPitch) ^ (dt * 32));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816<T>(acc[dt][nt], a, pb[mt][nt][0], pb[mt][nt][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) largest = max_magnitude<T>(largest, a[i]);
         }
+      if (!__any_sync(0xffffffffu, is_infinite<T>(largest))) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt) {
+            uint32_t a[4];
+            ldsm4_t(a, (v_at + mt * 16 * kPitch) ^ (dt * 32));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<T>(acc[dt][nt], a, rest[mt][nt][0], rest[mt][nt][1]);
+          }
       }
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;

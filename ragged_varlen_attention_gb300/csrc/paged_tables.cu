@@ -4,8 +4,9 @@
 //   old_b = ceil(len_b / P), need_b = ceil((len_b + n_b) / P) - old_b
 //   page i < need_b of request b is free[begin + sum_{a<b} need_a + i]
 //
-// A few integers per token: the launch latency bounds it, so it is one launch with no
-// step that waits for another block. Every block scans the need of all requests for
+// A few integers per token: the launch and three memory latencies in a row (lengths, page
+// number, slot) bound it, 3.9 us for 24 requests and 5.4 us for 512 requests with 65536 new
+// tokens, so it is one launch with no step that waits for another block. Every block scans the need of all requests for
 // itself (batch x 8 bytes from L2), and a token finds its page without the table being
 // written first: an old page from the table, a new one from the free list. The token
 // at the start of a new page writes the page's table entry, so nothing else has to.

@@ -8,9 +8,9 @@ that the tensor core adds in steps of 16 with at most a few truncated bits each,
 product with the scale: off by at most 64 u M. exp2 and the running rescaling add a few u
 each time a maximum moves, and a sum of n terms at most (n / 64 + 64) u: with
 e = 64 u M + (n / 64 + 96) u the weights p are off by e relative, and so is Stats, plus its
-own rounding, 4 u |Stats|. The matrix kernel rounds p to 16 bits (h, and half of float16's
-smallest step, 2^-25, for each key). So O is off by at most
-h |O| + (h16 + 2 e) sum_j p_j |v_j| + n 2^-25 max|v| (float16)."""
+own rounding, 4 u |Stats|. The matrix kernel takes p as two 16-bit parts (what is left is h^2,
+and half of float16's smallest step, 2^-25, for each key). So O is off by at most
+h |O| + (h^2 + 2 e) sum_j p_j |v_j| + n 2^-25 max|v| (float16)."""
 from __future__ import annotations
 
 import numpy as np
@@ -180,8 +180,8 @@ def check(cache, q, o, lse, scale=None, window=None, table=None, lens=None, o0=N
             m = abs(scale) * (np.abs(kk) @ np.abs(qn[b, h])).max()
             e = 64 * U * m + (len(keys) / 64 + 96) * U
             p = np.exp(scale * (kk @ qn[b, h]) - ref_lse[b, h])
-            h16 = HALF[dtype] if matrix else 0.0
-            bound = HALF[dtype] * np.abs(ref_o[b, h]) + (h16 + 2 * e) * (p @ vv)
+            rest = HALF[dtype] ** 2 if matrix else 0.0
+            bound = HALF[dtype] * np.abs(ref_o[b, h]) + (rest + 2 * e) * (p @ vv)
             if matrix and dtype == torch.float16:
                 bound = bound + len(keys) * 2.0 ** -25 * vv.max(0)
             if dtype == torch.float16:
