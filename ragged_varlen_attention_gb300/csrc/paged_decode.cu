@@ -17,13 +17,13 @@
 //     merges them in the line's order (no atomics: equal inputs give equal bits).
 //
 // Measured (both kernels), against a copy at 6.79 TB/s: bf16, 64 requests of 1 to 8192 keys, 32 + 8
-// heads of d = 128 (1.07 GB) 172 us (92 %); fp16, 2 x 131072 keys, 64 + 8 heads 167 us (95 %);
-// 1024 x 256 keys 186 us (85 %: a segment's beginning and end cost about a chunk's time each);
-// d = 64, one query head per kv head, pages of 24, a window of 1023 keys (142 MB) 35 us (60 %);
-// float32, 32 + 8 heads 176 us (90 %), 64 + 8 heads 245 us (65 %: bound by the fma and shuffles);
-// 16 heads a group, pages of one row 64 us for 254 MB (58 %). One request of 700 keys takes 7.8 us:
-// 2.5 us until each warp knows its range and 1.4 until its keys are there, 2 to compute, the rest in
-// the join kernel.
+// heads of d = 128 (1.07 GB) 169 us (94 %); fp16, 2 x 131072 keys, 64 + 8 heads 168 us (94 %);
+// 1024 x 256 keys 187 us (86 %: a segment's beginning and end cost about a chunk's time each);
+// d = 64, one query head per kv head, pages of 24, a window of 1023 keys (142 MB) 34 us (61 %);
+// 1.07 GB in pages of one row 206 us (77 %: every row's address by shuffles); float32, 32 + 8 heads
+// 174 us (91 %), 64 + 8 heads 243 us (65 %: bound by fma and shuffles). One request of 700 keys
+// takes 8.2 us: 0.85 for the launch, 1.1 until each warp knows its range, 0.9 until its keys are
+// there, 2.3 to compute and write, the rest in the join kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
