@@ -265,7 +265,9 @@ inline cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();  // reported by this call, not by a later one
+  return e;
 }
 
 // SM count of the current device (0: no device).
