@@ -165,7 +165,8 @@ def thd_paged_attention(q, k_cache, v_cache, block_table, seq_lens, *, window_le
     """One-call attention of one new token per request: Q [batch, h_q, d] against the
     ``seq_lens[b]`` cached keys of each request (int32 [batch], the new token's own among
     them), whose pages ``block_table`` (int32 [batch, max_pages]) names. ``window_left``
-    (int32 [batch], negative: none) bounds the keys from the left. Returns ``(o, stats)``."""
+    (int32 [batch], negative: none) bounds the keys from the left. For inference: no gradient
+    flows through it. Returns ``(o, stats)``."""
     _b._check_ints("seq_lens", seq_lens, (q.shape[0],))
     if window_left is not None:
         _b._check_ints("window_left", window_left, (q.shape[0],))
